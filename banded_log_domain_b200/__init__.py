@@ -68,6 +68,24 @@ class sa_shard(ctypes.Structure):
                 ("exchange", EXCHANGE_FN), ("user", ctypes.c_void_p)]
 
 
+_S3 = ctypes.c_longlong * 3
+
+
+class sa_softmax_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "Hq", "Hk", "Lq", "Lk", "d", "W")] + [
+        ("eps", ctypes.c_float), ("causal", ctypes.c_int), ("dtype", ctypes.c_int)] + [
+        (n + "_stride", _S3) for n in ("q", "k", "v", "o", "dO", "dq", "dk", "dv")]
+
+
+class sa_rotary_params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "Hq", "Hk", "L", "d", "rot", "interleaved")] + [
+        ("scale", ctypes.c_float), ("dtype", ctypes.c_int)] + [
+        (n + "_stride", _S3) for n in ("q", "k", "q_out", "k_out")]
+
+
+ROTARY_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+
+
 class LaunchTrace:
     """CUDA events recorded by the library around each of its kernel launches
     (the ``trace_*`` fields of ``sa_params``).  Pass as ``trace=`` to the
@@ -136,6 +154,20 @@ def _L():
                                               sz, vp]
     lib.sinkhorn_attn_strerror.argtypes = [ctypes.c_int]
     lib.sinkhorn_attn_strerror.restype = ctypes.c_char_p
+    SM, RP = ctypes.POINTER(sa_softmax_params), ctypes.POINTER(sa_rotary_params)
+    dbl = ctypes.c_double
+    lib.sinkhorn_attn_softmax_workspace_size.argtypes = [SM, ctypes.POINTER(sz), ctypes.POINTER(sz)]
+    lib.sinkhorn_attn_softmax_fwd.argtypes = [SM] + [vp] * 8 + [sz, vp]
+    lib.sinkhorn_attn_softmax_bwd.argtypes = [SM] + [vp] * 12 + [sz, vp]
+    lib.sinkhorn_attn_rotary_fwd.argtypes = [RP] + [vp] * 7
+    lib.sinkhorn_attn_rotary_bwd.argtypes = [RP] + [vp] * 7
+    lib.sinkhorn_attn_rotary_freqs.argtypes = [
+        ctypes.c_int, dbl, ctypes.c_int, dbl, dbl, dbl, dbl, ctypes.POINTER(dbl),
+        ctypes.POINTER(ctypes.c_float)]
+    for f in ("sinkhorn_attn_softmax_workspace_size", "sinkhorn_attn_softmax_fwd",
+              "sinkhorn_attn_softmax_bwd", "sinkhorn_attn_rotary_fwd", "sinkhorn_attn_rotary_bwd",
+              "sinkhorn_attn_rotary_freqs"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("sinkhorn_attn_state_size", "sinkhorn_attn_workspace_size", "sinkhorn_attn_fwd",
               "sinkhorn_attn_bwd", "sinkhorn_attn_debug_plan", "sinkhorn_attn_poll",
               "sinkhorn_attn_poll_static", "sinkhorn_attn_bias_certificate",
@@ -159,7 +191,10 @@ EXPORTS = ("sinkhorn_attn_state_size", "sinkhorn_attn_workspace_size", "sinkhorn
            "sinkhorn_attn_debug_timeout", "sinkhorn_attn_bias_certificate",
            "sinkhorn_attn_debug_exp2",
            "sinkhorn_attn_sq_dist", "sinkhorn_attn_fwd_sharded", "sinkhorn_attn_bwd_sharded",
-           "sinkhorn_attn_step_host_workspace_size", "sinkhorn_attn_step_host")
+           "sinkhorn_attn_step_host_workspace_size", "sinkhorn_attn_step_host",
+           "sinkhorn_attn_softmax_workspace_size", "sinkhorn_attn_softmax_fwd",
+           "sinkhorn_attn_softmax_bwd", "sinkhorn_attn_rotary_fwd", "sinkhorn_attn_rotary_bwd",
+           "sinkhorn_attn_rotary_freqs")
 
 
 def strerror(status: int) -> str:
@@ -190,6 +225,8 @@ def _stream(device):
 def _on(device, fn, *args):
     """Calls the C entry point ``fn`` with ``device`` current (the library
     validates every pointer against the current device and launches there)."""
+    if device.type == "cuda" and device.index == torch.cuda.current_device():
+        return fn(*args)
     with torch.cuda.device(device):
         return fn(*args)
 
@@ -614,3 +651,189 @@ def bias_certificate(q, k, v, dO, *, N, Rs=(0, 1, 2, 4), tau=1e-5, W, eps, mask=
            "sinkhorn_attn_bias_certificate")
     eta = {R: float(c_eta[i]) for i, R in enumerate(depths)}
     return eta, (None if c_rstar.value < 0 else int(c_rstar.value))
+
+
+# ---------------------------------------------------------------------------
+# softmax attention on the band, and rotary positions (see the C header)
+# ---------------------------------------------------------------------------
+
+_DTYPES = {torch.float32: SA_F32, torch.bfloat16: SA_BF16}
+
+
+def _strided(p, **tensors):
+    """Writes the tensors' batch, head and token strides into the params ``p``
+    (the library rejects those that are not multiples of 16 bytes)."""
+    for name, t in tensors.items():
+        st, n = t.stride(), t.shape
+        if st[3] != 1 and n[3] > 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+        if (st[0] <= 0 and n[0] > 1) or (st[1] <= 0 and n[1] > 1) or (st[2] <= 0 and n[2] > 1):
+            raise ValueError(f"{name}: expanded dimensions are not supported")
+        setattr(p, name + "_stride", _S3(*st[:3]))
+
+
+def _same(what, like, shape, **tensors):
+    """Every tensor of ``shape`` with ``like``'s dtype and device."""
+    for name, t in tensors.items():
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}, {what}")
+        if t.dtype != like.dtype or t.device != like.device:
+            raise ValueError(f"{name}: {t.dtype} on {t.device}, not {like.dtype} on {like.device}")
+
+
+def _aux(name, t, dtype, shape, device):
+    """An optional contiguous tensor of a fixed dtype and shape."""
+    if t is None:
+        return
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device:
+        raise ValueError(f"{name}: {dtype} {tuple(shape)} on {device} expected")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+
+
+def _softmax_params(q, k, v, W, eps, causal, mask, q_pos):
+    if q.dim() != 4 or k.dim() != 4 or not q.is_cuda or q.dtype not in _DTYPES:
+        raise ValueError("q, k, v are [B,H,L,64] float32 or bfloat16 CUDA tensors")
+    B, Hq, Lq, d = q.shape
+    Hk, Lk = k.shape[1], k.shape[2]
+    _same("as k", q, (B, Hk, Lk, d), k=k, v=v)
+    _aux("mask", mask, torch.uint8, (B, Lk), q.device)
+    _aux("q_pos", q_pos, torch.int32, (B,), q.device)
+    p = sa_softmax_params(B, Hq, Hk, Lq, Lk, d, min(int(W), 2**31 - 1), float(eps), int(bool(causal)),
+                          _DTYPES[q.dtype])
+    _strided(p, q=q, k=k, v=v)
+    return p
+
+
+def sinkhorn_attn_softmax_workspace_size(p: sa_softmax_params):
+    f, b = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(_L().sinkhorn_attn_softmax_workspace_size(ctypes.byref(p), ctypes.byref(f),
+                                                     ctypes.byref(b)), "softmax_workspace_size")
+    return f.value, b.value
+
+
+def _softmax_ws(p, ws, which, device):
+    if ws is None:
+        return torch.empty(sinkhorn_attn_softmax_workspace_size(p)[which], dtype=torch.uint8,
+                           device=device)
+    _contig(ws)
+    return ws
+
+
+def sinkhorn_attn_softmax_fwd(q, k, v, *, W, eps=1.0, causal=False, mask=None, q_pos=None, o=None,
+                              u=None, ws=None):
+    """Softmax attention on the band (the row half of one Sinkhorn iteration).
+    ``q``: ``[B,Hq,Lq,64]``, ``k, v``: ``[B,Hk,Lk,64]``, float32 or bfloat16 CUDA
+    tensors with any batch, head and token strides that are multiples of 16
+    bytes; ``Hq`` a multiple of ``Hk`` (shared key heads), ``Lq <= Lk``.  Query t
+    is the token at position ``q_pos[b] + t`` (int32 ``[B]``; None: the last
+    ``Lq``) and attends the keys within ``W`` positions (not the later ones when
+    ``causal``); ``mask``: ``[B,Lk]`` uint8 (1 = valid) or None.  Returns ``(o, u)``:
+    ``u`` is ``[B,Hq,Lq]`` float32, the row duals -log sum_j exp(S_ij)."""
+    p = _softmax_params(q, k, v, W, eps, causal, mask, q_pos)
+    dev = q.device
+    if o is None:
+        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    else:
+        _same("as q", q, q.shape, o=o)
+    _strided(p, o=o)
+    if u is None:
+        u = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
+    else:
+        _aux("u", u, torch.float32, q.shape[:3], dev)
+    ws = _softmax_ws(p, ws, 0, dev)
+    _check(_on(dev, _L().sinkhorn_attn_softmax_fwd, ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v),
+               _ptr(mask), _ptr(q_pos), _ptr(o), _ptr(u), _ptr(ws), ws.numel(), _stream(dev)),
+           "sinkhorn_attn_softmax_fwd")
+    return o, u
+
+
+def sinkhorn_attn_softmax_bwd(q, k, v, o, dO, u, *, W, eps=1.0, causal=False, mask=None,
+                              q_pos=None, dq=None, dk=None, dv=None, ws=None):
+    """Backward of <dO, O> of :func:`sinkhorn_attn_softmax_fwd`, which recomputes
+    the probabilities from the row duals ``u``.  Returns ``(dq, dk, dv)``, ``dk`` and
+    ``dv`` summed over the query heads that share a key head."""
+    p = _softmax_params(q, k, v, W, eps, causal, mask, q_pos)
+    dev = q.device
+    _same("as q", q, q.shape, o=o, dO=dO)
+    _aux("u", u, torch.float32, q.shape[:3], dev)
+    if dq is None:
+        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    if dk is None:
+        dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
+    if dv is None:
+        dv = torch.empty(k.shape, dtype=k.dtype, device=dev)
+    _same("as q", q, q.shape, dq=dq)
+    _same("as k", k, k.shape, dk=dk, dv=dv)
+    _strided(p, o=o, dO=dO, dq=dq, dk=dk, dv=dv)
+    ws = _softmax_ws(p, ws, 1, dev)
+    _check(_on(dev, _L().sinkhorn_attn_softmax_bwd, ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v),
+               _ptr(mask), _ptr(q_pos), _ptr(o), _ptr(dO), _ptr(u), _ptr(dq), _ptr(dk), _ptr(dv),
+               _ptr(ws), ws.numel(), _stream(dev)), "sinkhorn_attn_softmax_bwd")
+    return dq, dk, dv
+
+
+def sinkhorn_attn_rotary_freqs(rot, *, base=10000.0, scaling="plain", factor=1.0, train_len=0.0,
+                               turns=(32.0, 1.0), device="cuda"):
+    """Frequencies of ``rot`` rotated channels for :func:`sinkhorn_attn_rotary_fwd`:
+    ``(freqs, scale)``, ``freqs`` a float64 tensor ``[rot/2]`` on ``device`` (radians per
+    position) and ``scale`` the factor to pass along.  ``scaling``: "plain", or
+    stretched by ``factor`` for contexts longer than the trained one: "linear",
+    "ntk", "by_parts" (with ``train_len`` and ``turns``, see the C header)."""
+    n = max(int(rot) // 2, 1)
+    out, scale = (ctypes.c_double * n)(), ctypes.c_float(1.0)
+    _check(_L().sinkhorn_attn_rotary_freqs(int(rot), float(base), ROTARY_SCALINGS[scaling],
+                                           float(factor), float(train_len), float(turns[0]),
+                                           float(turns[1]), out, ctypes.byref(scale)),
+           "sinkhorn_attn_rotary_freqs")
+    return torch.tensor(list(out), dtype=torch.float64).to(device), scale.value
+
+
+def _rotary(entry, q, k, freqs, pos, interleaved, scale, q_out, k_out):
+    if q.dim() != 4 or not q.is_cuda or q.dtype not in _DTYPES:
+        raise ValueError("q, k are [B,H,L,d] float32 or bfloat16 CUDA tensors")
+    B, Hq, L, d = q.shape
+    dev, Hk = q.device, 0
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError("q, k are [B,H,L,d] float32 or bfloat16 CUDA tensors")
+        Hk = k.shape[1]
+        _same("as q, but for the heads", q, (B, Hk, L, d), k=k)
+    _aux("freqs", freqs, torch.float64, (freqs.numel(),), dev)
+    _aux("pos", pos, torch.int32, (B, L), dev)
+    p = sa_rotary_params(B, Hq, Hk, L, d, 2 * freqs.numel(), int(bool(interleaved)), float(scale),
+                         _DTYPES[q.dtype])
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    else:
+        _same("as q", q, q.shape, q_out=q_out)
+    _strided(p, q=q, q_out=q_out)
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        else:
+            _same("as k", k, k.shape, k_out=k_out)
+        _strided(p, k=k, k_out=k_out)
+    _check(_on(dev, getattr(_L(), entry), ctypes.byref(p), _ptr(freqs), _ptr(pos), _ptr(q), _ptr(k),
+               _ptr(q_out), _ptr(k_out if k is not None else None), _stream(dev)), entry)
+    return q_out, (k_out if k is not None else None)
+
+
+def sinkhorn_attn_rotary_fwd(q, k, freqs, *, pos=None, interleaved=False, scale=1.0, q_out=None,
+                             k_out=None):
+    """Rotary positions of ``q`` ``[B,Hq,L,d]`` and ``k`` ``[B,Hk,L,d]`` (or None), in one
+    launch.  The leading ``2 * len(freqs)`` channels are turned by ``pos[b,t] *
+    freqs`` (int32 ``[B,L]``; None: the token index) and multiplied by ``scale``, the
+    others copied; pairs are (i, i + rot/2), or (2i, 2i+1) when ``interleaved``.
+    Inputs may have any strides that are multiples of 16 bytes (a ``[B,L,H,d]``
+    projection transposed); new outputs are contiguous ``[B,H,L,d]``, the layout of
+    the attentions here.  An output may be its own input.  Returns
+    ``(q_out, k_out)``."""
+    return _rotary("sinkhorn_attn_rotary_fwd", q, k, freqs, pos, interleaved, scale, q_out, k_out)
+
+
+def sinkhorn_attn_rotary_bwd(dq, dk, freqs, *, pos=None, interleaved=False, scale=1.0, dq_in=None,
+                             dk_in=None):
+    """Backward of :func:`sinkhorn_attn_rotary_fwd`: the gradients of its inputs
+    from those of its outputs (the transposed rotation)."""
+    return _rotary("sinkhorn_attn_rotary_bwd", dq, dk, freqs, pos, interleaved, scale, dq_in, dk_in)

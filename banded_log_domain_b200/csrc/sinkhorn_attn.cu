@@ -30,6 +30,7 @@
 #include <type_traits>
 
 #include "../../include/sinkhorn_attn.h"
+#include "host_util.cuh"
 #include "simt_sweep.cuh"
 #include "tc_sweep.cuh"
 #include "tc_rowsum.cuh"
@@ -37,12 +38,9 @@
 namespace sa {
 namespace {
 
-constexpr size_t kHeader = 256;   // status word + padding at the start of every workspace
 constexpr int kD = simt::D;
 constexpr int kMaxR = 256;  // tail length limit (host term lists, workspace)
 constexpr int kMaxDevicesHS = 64;  // devices with copy streams for the host-buffer step
-
-size_t align_up(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct Dims {
     int B, H, L, R, ld, BH;
@@ -73,33 +71,6 @@ sa_status check_params(const sa_params* p, Dims* dd) {
     dd->ok = true;
     return SA_OK;
 }
-
-bool aligned16(const void* x) { return ((uintptr_t)x & 15u) == 0; }
-
-// Memory the current device's kernels may read and write at full speed: device
-// memory of the current device, or managed memory.  Pinned host memory (read
-// over PCIe), pageable host memory, and another device's memory (a tensor on
-// another GPU, or the wrong device current) are rejected before any launch.
-bool on_current_device(const void* x) {
-    cudaPointerAttributes at;
-    if (cudaPointerGetAttributes(&at, x) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    if (at.type == cudaMemoryTypeManaged) return true;
-    if (at.type != cudaMemoryTypeDevice) return false;
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    return at.device == dev;
-}
-bool device_ok(const void* x) { return x && aligned16(x) && on_current_device(x); }
-// A device float that may sit anywhere a float may (4-byte alignment).
-bool device_f32_ok(const void* x) { return x && ((uintptr_t)x & 3u) == 0 && on_current_device(x); }
-// The byte mask (any alignment; NULL means every token is valid).
-bool mask_ok(const void* x) { return !x || on_current_device(x); }
 
 // The row-sum sweeps on the tensor cores (bf16 storage without a dustbin) read
 // the duals as a working copy of the state: [BH][2R+2][L] float32, log2(e)
@@ -494,20 +465,6 @@ constexpr int kind_of(int mode) {
          : mode == simt::WSUM ? SA_KERNEL_WSUM : SA_KERNEL_DS;
 }
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link).
-PFN_cuTensorMapEncodeTiled_v12000 encode_tiled() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    return fn;
-}
-
 // [BH][L][64] bf16 viewed as a 3-D tensor; 64 x 128 x 1 boxes, 128-byte swizzle,
 // zero fill outside the tensor (rows < 0 or >= L).
 bool make_map(CUtensorMap* m, const void* ptr, int L, int BH) {
@@ -549,41 +506,6 @@ bool make_map_aug_strided(CUtensorMap* m, const void* ptr, int L, int BH, long l
               es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
            CUDA_SUCCESS;
-}
-
-// SMs of the device (persistent grids take one or two CTAs per SM); read once
-// from the first device asked, since the library targets a single GPU model
-// (sm_100a)
-int sm_count() {
-    static int nsm = 0;
-    if (nsm == 0) {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || nsm <= 0)
-            nsm = 148;
-    }
-    return nsm;
-}
-
-// Launches a persistent sweep with programmatic stream serialisation: its
-// CTAs may be placed while the previous kernel of the stream finishes, so their
-// set-up (barrier init, TMEM allocation) overlaps its tail; the sweeps wait for
-// that kernel (griddepcontrol.wait) before any global access, so the ordering
-// of their reads and writes is that of a plain launch.
-template <typename... Params, typename... Args>
-cudaError_t launch_pdl(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
-                       Args&&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
 template <int MODE, bool ONLINE, int NT>

@@ -1,0 +1,216 @@
+// C ABI of the softmax attention (sinkhorn_attn_softmax_*): argument
+// validation, the launch plan and the launches.
+#include <cmath>
+#include <algorithm>
+
+#include "host_util.cuh"
+#include "softmax.cuh"
+#include "softmax_simt.cuh"
+
+namespace sa {
+namespace {
+
+constexpr int kD = 64;
+constexpr int kMaxGroup = 64;   // query heads per key head (they share a tile's rows)
+
+// How a call is cut: query tiles of `nq` queries x the group's heads, the
+// forward's keys in `nsplit` parts per tile, each part in `nparts / nsplit`.
+struct Plan {
+    int G, nq, ntile, nktile, nsplit, nparts;
+    long long rows;  // B * Hq * Lq
+    size_t fwd_bytes, bwd_bytes, part_ml;
+};
+
+sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
+    if (!p) return SA_ERR_INVALID_ARG;
+    if (p->B < 0 || p->Hq < 0 || p->Hk < 0 || p->Lq < 0 || p->Lk < 0 || p->d <= 0 || p->W < 0)
+        return SA_ERR_INVALID_ARG;
+    if (!(p->eps > 0.f) || !std::isfinite(p->eps)) return SA_ERR_INVALID_ARG;
+    if (p->causal != 0 && p->causal != 1) return SA_ERR_INVALID_ARG;
+    if (p->dtype != SA_F32 && p->dtype != SA_BF16) return SA_ERR_INVALID_ARG;
+    if (p->Lq > p->Lk) return SA_ERR_INVALID_ARG;
+    if (p->Hk == 0 ? p->Hq != 0 : p->Hq % p->Hk != 0) return SA_ERR_INVALID_ARG;
+    if (p->d != kD) return SA_ERR_UNSUPPORTED;
+    pl->G = p->Hk ? std::max(1, p->Hq / p->Hk) : 1;
+    if (pl->G > kMaxGroup) return SA_ERR_UNSUPPORTED;
+    // token indices stay clear of 2^31 with a tile's rows added
+    if (p->Lk > (1 << 30) || (long long)p->B * p->Hq > 65535) return SA_ERR_UNSUPPORTED;
+    pl->rows = (long long)p->B * p->Hq * p->Lq;
+    const int M = 64, N = 64;  // rows of a tile, keys of a chunk
+    pl->nq = M / pl->G;
+    pl->ntile = (p->Lq + pl->nq - 1) / pl->nq;
+    pl->nktile = (p->Lk + 63) / 64;
+    // A few query rows over many keys (single new tokens) would leave most SMs
+    // idle: then every tile's keys are cut into parts for about two blocks an
+    // SM, of at least four chunks each, joined by a second kernel.
+    const long long tiles = (long long)p->B * p->Hk * pl->ntile;
+    if (std::max(tiles, (long long)p->B * p->Hk * pl->nktile) > (1LL << 30)) return SA_ERR_UNSUPPORTED;
+    const long long W = std::min(p->W, p->Lk);
+    const long long keys = std::min<long long>(p->Lk, W + (p->causal ? 0 : W) + pl->nq);
+    const long long chunks = (keys + N - 1) / N;
+    pl->nsplit = 1;
+    if (tiles > 0 && tiles < sm_count())
+        pl->nsplit = (int)std::max<long long>(1, std::min((2LL * sm_count() + tiles - 1) / tiles, chunks / 4));
+    pl->nparts = pl->nsplit;
+    const long long parts = pl->nsplit > 1 ? pl->rows * pl->nparts : 0;
+    pl->part_ml = kHeader + align_up((size_t)parts * kD * 4);
+    pl->fwd_bytes = pl->part_ml + align_up((size_t)parts * 8);
+    pl->bwd_bytes = kHeader + align_up((size_t)pl->rows * 4);
+    return SA_OK;
+}
+
+// A [B][H][L][64] tensor's strides (three zeros: contiguous); false unless each
+// is a positive multiple of 16 bytes (extents of 1 are not looked at).
+bool view(sm::View* v, const void* ptr, const long long s[3], int B, int H, int L, int size) {
+    v->p = const_cast<void*>(ptr);
+    if (!s[0] && !s[1] && !s[2]) {
+        v->s[2] = kD;
+        v->s[1] = (long long)L * kD;
+        v->s[0] = (long long)H * L * kD;
+        return true;
+    }
+    const long long n[3] = {B, H, L};
+    for (int i = 0; i < 3; ++i) {
+        v->s[i] = n[i] > 1 ? s[i] : 0;
+        if (n[i] > 1 && (s[i] <= 0 || (s[i] * size) % 16 != 0 || s[i] > (1LL << 38))) return false;
+    }
+    return true;
+}
+
+bool ints_ok(const int* x) { return !x || (((uintptr_t)x & 3u) == 0 && on_current_device(x)); }
+
+template <typename K>
+cudaError_t launch(K kern, long long grid, int threads, int smem, cudaStream_t st, const sm::Args& a) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    kern<<<(unsigned)grid, threads, smem, st>>>(a);
+    return cudaGetLastError();
+}
+
+void base_args(sm::Args* a, const sa_softmax_params* p, const Plan& pl, const uint8_t* mask, const int* q_pos,
+               void* ws) {
+    a->B = p->B;
+    a->Hq = p->Hq;
+    a->Hk = p->Hk;
+    a->G = pl.G;
+    a->Lq = p->Lq;
+    a->Lk = p->Lk;
+    a->W = std::min(p->W, p->Lk);
+    a->R = p->causal ? 0 : a->W;
+    a->c = 1.0f / (std::sqrt((float)p->d) * p->eps);
+    a->c2 = a->c * kLog2e;
+    a->q_pos = q_pos;
+    a->mask = mask;
+    a->status = (int*)ws;
+    a->nq = pl.nq;
+    a->ntile = pl.ntile;
+    a->nsplit = 1;
+    a->nparts = 1;
+    a->exact_d = 0;
+}
+
+template <typename T>
+cudaError_t fwd_launch(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
+    const long long tiles = (long long)p->B * p->Hk * pl.ntile;
+    cudaError_t e = launch(sm::simt::k_fwd<T>, tiles * pl.nsplit, sm::simt::THREADS, sm::simt::smem_bytes(4), st, a);
+    if (e == cudaSuccess && pl.nsplit > 1) e = launch(sm::k_join<T>, (pl.rows + 3) / 4, 128, 0, st, a);
+    return e;
+}
+
+template <typename T>
+cudaError_t bwd_launch(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cudaStream_t st) {
+    const long long tiles = (long long)p->B * p->Hk * pl.ntile;
+    if (pl.rows > 0) {
+        const cudaError_t e = launch(sm::simt::k_bwd_q<T>, tiles, sm::simt::THREADS, sm::simt::smem_bytes(5), st, a);
+        if (e != cudaSuccess) return e;
+    } else {
+        a.Lq = 0;  // no query: the key sweep writes zeros
+    }
+    a.ntile = pl.nktile;
+    return launch(sm::simt::k_bwd_kv<T>, (long long)p->B * p->Hk * pl.nktile, sm::simt::THREADS,
+                  sm::simt::smem_bytes(6), st, a);
+}
+
+}  // namespace
+}  // namespace sa
+
+extern "C" {
+
+sa_status sinkhorn_attn_softmax_workspace_size(const sa_softmax_params* p, size_t* fwd_bytes, size_t* bwd_bytes) {
+    sa::Plan pl;
+    const sa_status s = sa::make_plan(p, &pl);
+    if (s != SA_OK) return s;
+    if (fwd_bytes) *fwd_bytes = pl.fwd_bytes;
+    if (bwd_bytes) *bwd_bytes = pl.bwd_bytes;
+    return SA_OK;
+}
+
+sa_status sinkhorn_attn_softmax_fwd(const sa_softmax_params* p, const void* q, const void* k, const void* v,
+                                    const uint8_t* mask, const int* q_pos, void* o, float* u, void* ws,
+                                    size_t ws_bytes, void* stream) {
+    using namespace sa;
+    Plan pl;
+    const sa_status s = make_plan(p, &pl);
+    if (s != SA_OK) return s;
+    if (ws_bytes < pl.fwd_bytes) return SA_ERR_WORKSPACE;
+    const int size = p->dtype == SA_F32 ? 4 : 2;
+    sm::Args a;
+    base_args(&a, p, pl, mask, q_pos, ws);
+    if (!view(&a.q, q, p->q_stride, p->B, p->Hq, p->Lq, size) || !view(&a.k, k, p->k_stride, p->B, p->Hk, p->Lk, size) ||
+        !view(&a.v, v, p->v_stride, p->B, p->Hk, p->Lk, size) || !view(&a.o, o, p->o_stride, p->B, p->Hq, p->Lq, size))
+        return SA_ERR_INVALID_ARG;
+    if (pl.rows == 0) return SA_OK;
+    if (!device_ok(q) || !device_ok(k) || !device_ok(v) || !device_ok(o) || !device_ok(u) || !device_ok(ws) ||
+        !mask_ok(mask) || !ints_ok(q_pos))
+        return SA_ERR_INVALID_ARG;
+    a.u = u;
+    a.nsplit = pl.nsplit;
+    a.nparts = pl.nparts;
+    a.part_o = (float*)((char*)ws + kHeader);
+    a.part_ml = (float2*)((char*)ws + pl.part_ml);
+    const cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e =
+        p->dtype == SA_F32 ? fwd_launch<float>(p, pl, a, st) : fwd_launch<__nv_bfloat16>(p, pl, a, st);
+    return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+sa_status sinkhorn_attn_softmax_bwd(const sa_softmax_params* p, const void* q, const void* k, const void* v,
+                                    const uint8_t* mask, const int* q_pos, const void* o, const void* dO,
+                                    const float* u, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                                    void* stream) {
+    using namespace sa;
+    Plan pl;
+    const sa_status s = make_plan(p, &pl);
+    if (s != SA_OK) return s;
+    if (ws_bytes < pl.bwd_bytes) return SA_ERR_WORKSPACE;
+    const int size = p->dtype == SA_F32 ? 4 : 2;
+    sm::Args a;
+    base_args(&a, p, pl, mask, q_pos, ws);
+    if (!view(&a.q, q, p->q_stride, p->B, p->Hq, p->Lq, size) || !view(&a.k, k, p->k_stride, p->B, p->Hk, p->Lk, size) ||
+        !view(&a.v, v, p->v_stride, p->B, p->Hk, p->Lk, size) || !view(&a.o, o, p->o_stride, p->B, p->Hq, p->Lq, size) ||
+        !view(&a.dO, dO, p->dO_stride, p->B, p->Hq, p->Lq, size) ||
+        !view(&a.dq, dq, p->dq_stride, p->B, p->Hq, p->Lq, size) ||
+        !view(&a.dk, dk, p->dk_stride, p->B, p->Hk, p->Lk, size) ||
+        !view(&a.dv, dv, p->dv_stride, p->B, p->Hk, p->Lk, size))
+        return SA_ERR_INVALID_ARG;
+    if ((long long)p->B * p->Hk * p->Lk == 0) return SA_OK;
+    if (!device_ok(k) || !device_ok(v) || !device_ok(dk) || !device_ok(dv) || !device_ok(ws) || !mask_ok(mask) ||
+        !ints_ok(q_pos))
+        return SA_ERR_INVALID_ARG;
+    if (pl.rows > 0 && (!device_ok(q) || !device_ok(o) || !device_ok(dO) || !device_ok(u) || !device_ok(dq)))
+        return SA_ERR_INVALID_ARG;
+    a.u = const_cast<float*>(u);
+    a.D = (float*)((char*)ws + kHeader);
+    // With few keys a row's probabilities are large and dO . O, taken from the
+    // rounded O, is off by about as much as the dS it is subtracted in: up to
+    // 64 keys the sweep forms D itself, in a pass of its own over them.
+    a.exact_d = p->dtype == SA_BF16 && (long long)a.W + a.R + 1 <= 64;
+    const cudaStream_t st = (cudaStream_t)stream;
+    const cudaError_t e =
+        p->dtype == SA_F32 ? bwd_launch<float>(p, pl, a, st) : bwd_launch<__nv_bfloat16>(p, pl, a, st);
+    return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
+}  // extern "C"

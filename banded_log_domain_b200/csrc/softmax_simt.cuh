@@ -1,0 +1,409 @@
+// Softmax attention on the FP32 pipe: 64 x 64 tiles, 256 threads of 4 x 4
+// entries.  All products are packed f32x2 FMAs on operands in shared memory.
+// Bound by FFMA issue and the shared-memory reads that feed it.
+#pragma once
+
+#include "softmax.cuh"
+#include "tc_ptx.cuh"
+
+namespace sa {
+namespace sm {
+namespace simt {
+
+constexpr int LD = 68;            // floats per tile row: 16-byte aligned, rows 4 banks apart
+constexpr int TILE = 64 * LD;     // floats of a 64 x 64 tile
+constexpr int THREADS = 256;
+
+__host__ __device__ constexpr int smem_bytes(int tiles) { return tiles * TILE * 4; }
+
+// acc[i][j] += sum_k A[ty * 4 + i][k] B[tx + 16 j][k] (k pairs summed apart, then together)
+__device__ __forceinline__ void mm_abt(const float* A, const float* B, int ty, int tx, float (&s)[4][4]) {
+    uint64_t acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0;
+#pragma unroll 4
+    for (int k = 0; k < 64; k += 4) {
+        ulonglong2 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const ulonglong2*>(A + (ty * 4 + i) * LD + k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const ulonglong2*>(B + (tx + 16 * j) * LD + k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[i][j] = tc::fma2(x[i].x, y[j].x, acc[i][j]);
+                acc[i][j] = tc::fma2(x[i].y, y[j].y, acc[i][j]);
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float lo, hi;
+            tc::upk2(acc[i][j], lo, hi);
+            s[i][j] = lo + hi;
+        }
+}
+
+// acc[i][0..3] (two packed pairs) += sum_j P[ty * 4 + i][j] X[j][tx * 4 ..]
+__device__ __forceinline__ void mm_ab(const float* P, const float* X, int ty, int tx, uint64_t (&acc)[4][2]) {
+#pragma unroll 4
+    for (int j = 0; j < 64; j += 4) {
+        float4 p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(P + (ty * 4 + i) * LD + j);
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+            const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(X + (j + jj) * LD + tx * 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float e = reinterpret_cast<const float*>(&p[i])[jj];
+                const uint64_t ee = tc::pk2(e, e);
+                acc[i][0] = tc::fma2(ee, x.x, acc[i][0]);
+                acc[i][1] = tc::fma2(ee, x.y, acc[i][1]);
+            }
+        }
+    }
+}
+
+// One 64 x 64 tile of rows base(r) (nullptr: zeros) into shared memory as float.
+template <typename T, typename F>
+__device__ __forceinline__ void load_tile(float* dst, F base) {
+    constexpr int V = 16 / sizeof(T), PER = 64 / V;
+#pragma unroll
+    for (int x = threadIdx.x; x < 64 * PER; x += THREADS) {
+        const int r = x / PER, c = (x % PER) * V;
+        const T* p = base(r);
+        float e[V];
+        if (p) load_vec(p + c, e, V);
+        else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) e[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+            *reinterpret_cast<float4*>(dst + r * LD + c + i) = make_float4(e[i], e[i + 1], e[i + 2], e[i + 3]);
+    }
+}
+
+__device__ __forceinline__ float sum16(float x) {
+#pragma unroll
+    for (int m = 8; m; m >>= 1) x += __shfl_xor_sync(~0u, x, m);
+    return x;
+}
+__device__ __forceinline__ float max16(float x) {
+#pragma unroll
+    for (int m = 8; m; m >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, m));
+    return x;
+}
+
+// A tile of query rows: which query and head a row is, and the keys it attends.
+struct RowTile {
+    int b, hk, i0, part;
+    long long first;
+    int lo[4], hi[4];  // this thread's four rows (hi < lo: none)
+    int jlo, jhi;      // the tile's keys
+
+    __device__ void init(const Args& a, int ty) {
+        int x = blockIdx.x;
+        part = x % a.nsplit;
+        x /= a.nsplit;
+        const int qt = x % a.ntile;
+        x /= a.ntile;
+        hk = x % a.Hk;
+        b = x / a.Hk;
+        i0 = qt * a.nq;
+        first = a.first(b);
+        tile_keys(a, first, i0, min(i0 + a.nq, a.Lq) - 1, jlo, jhi);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            int h, t;
+            lo[i] = 0;
+            hi[i] = -1;
+            if (!row(a, ty * 4 + i, h, t)) continue;
+            const long long p = first + t;
+            if (p >= 0 && p < a.Lk && a.live(b, (int)p)) a.keys(p, lo[i], hi[i]);
+        }
+    }
+    __device__ __forceinline__ bool row(const Args& a, int r, int& h, int& t) const {
+        const int g = r / a.nq;
+        t = i0 + r % a.nq;
+        h = hk * a.G + g;
+        return g < a.G && t < a.Lq;
+    }
+};
+
+// Which of the chunk's 64 keys exist and are unmasked, as two words.
+__device__ __forceinline__ void live_keys(const Args& a, int b, int c0, uint32_t* words) {
+    if (threadIdx.x < 64) {
+        const int j = c0 + threadIdx.x;
+        const bool ok = j < a.Lk && a.live(b, j);
+        const uint32_t w = __ballot_sync(~0u, ok);
+        if ((threadIdx.x & 31) == 0) words[threadIdx.x >> 5] = w;
+    }
+}
+__device__ __forceinline__ bool live_bit(const uint32_t* words, int j) { return (words[j >> 5] >> (j & 31)) & 1u; }
+
+// One pass over the keys with the running maximum and sum of each row.
+template <typename T>
+__global__ void __launch_bounds__(THREADS) k_fwd(const Args a) {
+    extern __shared__ __align__(16) float sh[];
+    __shared__ uint32_t words[2];
+    float *Q = sh, *K = Q + TILE, *V = K + TILE, *P = V + TILE;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+    RowTile rt;
+    rt.init(a, ty);
+    const int n = (rt.jhi - rt.jlo + 64) / 64;  // 0 when empty
+    const int n0 = (int)((long long)n * rt.part / a.nsplit), n1 = (int)((long long)n * (rt.part + 1) / a.nsplit);
+    load_tile<T>(Q, [&](int r) -> const T* {
+        int h, t;
+        return rt.row(a, r, h, t) ? a.q.at<T>(rt.b, h, t) : nullptr;
+    });
+    float m[4], l[4];
+    uint64_t o[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+        o[i][0] = o[i][1] = 0;
+    }
+    for (int ch = n0; ch < n1; ++ch) {
+        const int c0 = rt.jlo + 64 * ch;
+        __syncthreads();
+        live_keys(a, rt.b, c0, words);
+        auto row = [&](const View& x, int r) -> const T* {
+            const int j = c0 + r;
+            return j <= rt.jhi && a.live(rt.b, j) ? x.at<T>(rt.b, rt.hk, j) : nullptr;
+        };
+        load_tile<T>(K, [&](int r) { return row(a.k, r); });
+        load_tile<T>(V, [&](int r) { return row(a.v, r); });
+        __syncthreads();
+        float s[4][4];
+        mm_abt(Q, K, ty, tx, s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float top = m[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int jj = tx + 16 * j, key = c0 + jj;
+                const bool on = key >= rt.lo[i] && key <= rt.hi[i] && live_bit(words, jj);
+                s[i][j] = on ? s[i][j] * a.c2 : -INFINITY;
+                top = fmaxf(top, s[i][j]);
+            }
+            top = max16(top);
+            const float use = top == -INFINITY ? 0.f : top;
+            const float f = ex2(m[i] - use);
+            m[i] = top;
+            float add = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = ex2(s[i][j] - use);
+                add += p;
+                P[(ty * 4 + i) * LD + tx + 16 * j] = p;
+            }
+            l[i] = l[i] * f + add;  // this thread's share of the sum
+            const uint64_t ff = tc::pk2(f, f);
+            o[i][0] = tc::fma2(o[i][0], ff, 0);
+            o[i][1] = tc::fma2(o[i][1], ff, 0);
+        }
+        __syncwarp();  // a warp writes and reads the same rows of P
+        mm_ab(P, V, ty, tx, o);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float total = sum16(l[i]);
+        int h, t;
+        if (!rt.row(a, ty * 4 + i, h, t)) continue;
+        float x[4];
+        tc::upk2(o[i][0], x[0], x[1]);
+        tc::upk2(o[i][1], x[2], x[3]);
+        const long long row = ((long long)rt.b * a.Hq + h) * a.Lq + t;
+        if (a.nsplit > 1) {
+            const long long at = row * a.nparts + rt.part;
+            store4(a.part_o + at * 64 + tx * 4, x[0], x[1], x[2], x[3]);
+            if (tx == 0) a.part_ml[at] = make_float2(m[i], total);
+            continue;
+        }
+        const float inv = total == 0.f ? 0.f : 1.f / total;  // a NaN stays one
+        store4(a.o.at<T>(rt.b, h, t) + tx * 4, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+        if (tx == 0) a.u[row] = total == 0.f ? 0.f : -(m[i] + lg2(total)) * kLn2;
+    }
+}
+
+// dQ by query rows; also D, for the key sweep.
+template <typename T>
+__global__ void __launch_bounds__(THREADS) k_bwd_q(const Args a) {
+    extern __shared__ __align__(16) float sh[];
+    __shared__ uint32_t words[2];
+    float *Q = sh, *dO = Q + TILE, *K = dO + TILE, *V = K + TILE, *S = V + TILE;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+    RowTile rt;
+    rt.init(a, ty);
+    const int n = (rt.jhi - rt.jlo + 64) / 64;
+    auto qrow = [&](const View& x, int r) -> const T* {
+        int h, t;
+        if (!rt.row(a, r, h, t)) return nullptr;
+        const long long p = rt.first + t;
+        return p >= 0 && p < a.Lk && a.live(rt.b, (int)p) ? x.at<T>(rt.b, h, t) : nullptr;
+    };
+    load_tile<T>(Q, [&](int r) { return qrow(a.q, r); });
+    load_tile<T>(dO, [&](int r) { return qrow(a.dO, r); });
+    __syncthreads();
+    float u2[4], D[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        u2[i] = D[i] = 0.f;
+        int h, t;
+        if (!rt.row(a, ty * 4 + i, h, t)) h = -1;
+        if (h >= 0) u2[i] = a.u[((long long)rt.b * a.Hq + h) * a.Lq + t] * kLog2e;
+        if (!a.exact_d) {
+            float dot = 0.f;
+            if (const T* o = qrow(a.o, ty * 4 + i)) {
+                const float* g = dO + (ty * 4 + i) * LD + tx * 4;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dot = fmaf(to_f32(o[tx * 4 + e]), g[e], dot);
+            }
+            D[i] = sum16(dot);
+        }
+    }
+    uint64_t acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = 0;
+    // with exact_d the keys are walked twice: first D = sum_j P <dO, V_j>, then dQ
+    const int first_pass = a.exact_d ? n : 0;
+    for (int x = 0; x < n + first_pass; ++x) {
+        const bool sum = x < first_pass;
+        const int c0 = rt.jlo + 64 * (sum ? x : x - first_pass);
+        __syncthreads();
+        live_keys(a, rt.b, c0, words);
+        auto row = [&](const View& y, int r) -> const T* {
+            const int j = c0 + r;
+            return j <= rt.jhi && a.live(rt.b, j) ? y.at<T>(rt.b, rt.hk, j) : nullptr;
+        };
+        load_tile<T>(K, [&](int r) { return row(a.k, r); });
+        load_tile<T>(V, [&](int r) { return row(a.v, r); });
+        __syncthreads();
+        float s[4][4], g[4][4];
+        mm_abt(Q, K, ty, tx, s);
+        mm_abt(dO, V, ty, tx, g);
+        if (a.exact_d && x == first_pass) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) D[i] = sum16(D[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int jj = tx + 16 * j, key = c0 + jj;
+                const bool on = key >= rt.lo[i] && key <= rt.hi[i] && live_bit(words, jj);
+                const float p = on ? ex2(fmaf(s[i][j], a.c2, u2[i])) : 0.f;
+                if (sum) D[i] += on ? p * g[i][j] : 0.f;
+                else S[(ty * 4 + i) * LD + jj] = on ? p * (g[i][j] - D[i]) : 0.f;
+            }
+        if (sum) continue;
+        __syncwarp();
+        mm_ab(S, K, ty, tx, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int h, t;
+        if (!rt.row(a, ty * 4 + i, h, t)) continue;
+        float x[4];
+        tc::upk2(acc[i][0], x[0], x[1]);
+        tc::upk2(acc[i][1], x[2], x[3]);
+        store4(a.dq.at<T>(rt.b, h, t) + tx * 4, x[0] * a.c, x[1] * a.c, x[2] * a.c, x[3] * a.c);
+        if (tx == 0) a.D[((long long)rt.b * a.Hq + h) * a.Lq + t] = D[i];
+    }
+}
+
+// dK and dV by key rows: the queries of every head of the group whose band holds the keys.
+template <typename T>
+__global__ void __launch_bounds__(THREADS) k_bwd_kv(const Args a) {
+    extern __shared__ __align__(16) float sh[];
+    __shared__ uint32_t words[2];
+    __shared__ float u2[64], D[64];
+    float *K = sh, *V = K + TILE, *Q = V + TILE, *dO = Q + TILE, *P = dO + TILE, *S = P + TILE;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    int x = blockIdx.x;
+    const int j0 = (x % a.ntile) * 64;
+    x /= a.ntile;
+    const int hk = x % a.Hk, b = x / a.Hk;
+    const long long first = a.first(b);
+    // queries whose position lies in [j0 - R, j0 + 63 + W] and in the sequence
+    const long long pl = j0 - (long long)a.R > 0 ? j0 - (long long)a.R : 0;
+    const long long ph = (long long)j0 + 63 + a.W < a.Lk - 1 ? (long long)j0 + 63 + a.W : a.Lk - 1;
+    const long long il = pl - first > 0 ? pl - first : 0;
+    const long long ih = ph - first < a.Lq - 1 ? ph - first : a.Lq - 1;
+    const int n = ih < il ? 0 : (int)((ih - il) / 64 + 1);
+    auto krow = [&](const View& y, int r) -> const T* {
+        const int j = j0 + r;
+        return j < a.Lk && a.live(b, j) ? y.at<T>(b, hk, j) : nullptr;
+    };
+    load_tile<T>(K, [&](int r) { return krow(a.k, r); });
+    load_tile<T>(V, [&](int r) { return krow(a.v, r); });
+    bool ok[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ok[i] = krow(a.k, ty * 4 + i) != nullptr;
+    uint64_t dk[4][2], dv[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dk[i][0] = dk[i][1] = dv[i][0] = dv[i][1] = 0;
+    for (int y = 0; y < n * a.G; ++y) {
+        const int h = hk * a.G + y / n;
+        const int t0 = (int)il + 64 * (y % n);
+        __syncthreads();
+        if (threadIdx.x < 64) {
+            const int t = t0 + threadIdx.x;
+            const bool on = t <= ih && a.live(b, (int)(first + t));
+            const uint32_t w = __ballot_sync(~0u, on);
+            if ((threadIdx.x & 31) == 0) words[threadIdx.x >> 5] = w;
+            const long long at = ((long long)b * a.Hq + h) * a.Lq + t;
+            u2[threadIdx.x] = on ? a.u[at] * kLog2e : 0.f;
+            D[threadIdx.x] = on ? a.D[at] : 0.f;
+        }
+        auto row = [&](const View& z, int r) -> const T* {
+            const int t = t0 + r;
+            return t <= ih && a.live(b, (int)(first + t)) ? z.at<T>(b, h, t) : nullptr;
+        };
+        load_tile<T>(Q, [&](int r) { return row(a.q, r); });
+        load_tile<T>(dO, [&](int r) { return row(a.dO, r); });
+        __syncthreads();
+        float s[4][4], g[4][4];
+        mm_abt(K, Q, ty, tx, s);
+        mm_abt(V, dO, ty, tx, g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int jj = tx + 16 * j;
+                const long long gap = first + t0 + jj - (j0 + ty * 4 + i);  // query's position less the key's
+                const bool on = ok[i] && live_bit(words, jj) && gap <= a.W && gap >= -(long long)a.R;
+                const float p = on ? ex2(fmaf(s[i][j], a.c2, u2[jj])) : 0.f;
+                P[(ty * 4 + i) * LD + jj] = p;
+                S[(ty * 4 + i) * LD + jj] = on ? p * (g[i][j] - D[jj]) : 0.f;
+            }
+        __syncwarp();
+        mm_ab(P, dO, ty, tx, dv);
+        mm_ab(S, Q, ty, tx, dk);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int j = j0 + ty * 4 + i;
+        if (j >= a.Lk) continue;
+        float z[4];
+        tc::upk2(dv[i][0], z[0], z[1]);
+        tc::upk2(dv[i][1], z[2], z[3]);
+        store4(a.dv.at<T>(b, hk, j) + tx * 4, z[0], z[1], z[2], z[3]);
+        tc::upk2(dk[i][0], z[0], z[1]);
+        tc::upk2(dk[i][1], z[2], z[3]);
+        store4(a.dk.at<T>(b, hk, j) + tx * 4, z[0] * a.c, z[1] * a.c, z[2] * a.c, z[3] * a.c);
+    }
+}
+
+}  // namespace simt
+}  // namespace sm
+}  // namespace sa

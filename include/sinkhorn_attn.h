@@ -363,6 +363,123 @@ sa_status sinkhorn_attn_bias_certificate(int n_depths, const int* depths, int n_
                                          const double* sums, double tau, double* eta,
                                          int* r_star);
 
+/*
+ * Softmax attention on the same band (no counterpart in the pages, whose
+ * comparison partner it is): the row half of one Sinkhorn iteration from v = 0,
+ *     u_i = -log sum_{j in Omega_i} exp(S_ij),   O_i = sum_j exp(S_ij + u_i) V_j,
+ * with S_ij = <q_i, k_j> / (sqrt(d) * eps) as above and the backward of <dO, O>
+ * that recomputes P_ij = exp(S_ij + u_i) from the row dual:
+ *     D_i = sum_j P_ij <dO_i, V_j>,   dS = P (dO V^T - D),
+ *     dQ = c dS K,   dK = c dS^T Q,   dV = P^T dO,   c = 1 / (sqrt(d) * eps).
+ * Queries are tokens: query t of sequence b is the token at position
+ * p = q_pos[b] + t of the Lk keys (q_pos NULL: the last Lq of them,
+ * p = Lk - Lq + t), and attends the keys
+ *     Omega = { j : p - W <= j <= p + W  (j <= p when causal),  0 <= j < Lk,
+ *               mask[b][j] = 1 and mask[b][p] = 1 }.
+ * Hq query heads share Hk key and value heads: query head h reads key head
+ * h / (Hq / Hk), and dK, dV are summed over the query heads that share one.
+ * Lq = 1 with q_pos = (tokens held) - 1 is the step of a single new token over
+ * a cache of capacity Lk.  A row with no key (masked, at a position outside
+ * [0, Lk), or whose band is masked out) has O, u, dQ exactly 0; a key that no
+ * query attends has dK, dV exactly 0.
+ *   - Q, O, dO, dQ are [B][Hq][Lq][d]; K, V, dK, dV [B][Hk][Lk][d]; each with
+ *     element strides for batch, head and token (x_stride; three zeros:
+ *     contiguous; the stride of an extent of 1 is not read), positive
+ *     multiples of 16 bytes, d contiguous.  Tensors written must not overlap
+ *     themselves or each other.  u is contiguous [B][Hq][Lq].
+ *   - The contents of masked tokens, and of keys outside every band of the call
+ *     (the unwritten tail of a cache), are not used, whatever they hold.  A
+ *     non-finite value of a token in use reaches the rows that attend it and
+ *     may reach others whose tokens lie within 255 positions of those.
+ *   - Results do not depend on the order in which blocks run (no atomics).
+ *   - The workspace needs no initialisation: every call resets the status word
+ *     at its start (read it with sinkhorn_attn_poll), so calls on two streams
+ *     at once, or captured into graphs that may run at once, need one each.
+ */
+typedef struct {
+    int B, Hq, Hk, Lq, Lk, d;  /* d == 64, Hq a multiple of Hk, Hq / Hk <= 64, Lq <= Lk */
+    int W;                     /* band half-width, W >= 0 (W >= Lk - 1 is dense) */
+    float eps;                 /* temperature, > 0 */
+    int causal;                /* 0 or 1: keys at later positions are left out */
+    sa_dtype dtype;            /* element type of Q, K, V, O, dO, dQ, dK, dV */
+    long long q_stride[3], k_stride[3], v_stride[3], o_stride[3];
+    long long dO_stride[3], dq_stride[3], dk_stride[3], dv_stride[3];
+} sa_softmax_params;
+
+/* Workspace bytes of the two calls below (either pointer may be NULL).  The
+ * forward's holds partial rows where few queries have their keys split over
+ * several blocks (at most 37 MB); the backward's one float32 per query row. */
+sa_status sinkhorn_attn_softmax_workspace_size(const sa_softmax_params* p, size_t* fwd_bytes,
+                                               size_t* bwd_bytes);
+
+/* Forward.  mask: [B][Lk] uint8, device, or NULL (all valid); q_pos: [B] int32,
+ * device, or NULL; o and u (float32) written. */
+sa_status sinkhorn_attn_softmax_fwd(const sa_softmax_params* p, const void* q, const void* k,
+                                    const void* v, const uint8_t* mask, const int* q_pos, void* o,
+                                    float* u, void* ws, size_t ws_bytes, void* stream);
+
+/* Backward.  q, k, v, mask, q_pos as given to the forward, o and u its outputs;
+ * dq, dk, dv written. */
+sa_status sinkhorn_attn_softmax_bwd(const sa_softmax_params* p, const void* q, const void* k,
+                                    const void* v, const uint8_t* mask, const int* q_pos,
+                                    const void* o, const void* dO, const float* u, void* dq,
+                                    void* dk, void* dv, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Rotary positions of queries and keys before either attention (no counterpart
+ * in the pages).  Channel pair i < rot / 2 of the token at position p is turned
+ * by the angle p * freqs[i] and multiplied by scale:
+ *     y_a = scale (x_a cos - x_b sin),   y_b = scale (x_a sin + x_b cos),
+ * (a, b) = (i, i + rot/2), or (2i, 2i + 1) when interleaved; channels rot .. d-1
+ * are copied.  The angle is formed and reduced in double, so positions up to
+ * 2^31 - 1 keep float32 accuracy.  The backward is the transpose (the angle
+ * negated) of the gradients.  One launch turns both tensors.
+ *   - Inputs and outputs are [B][H][L][d] with strides as above (three zeros:
+ *     contiguous), so a [B][L][H][d] projection can be read in place and
+ *     written in the layout that sinkhorn_attn_fwd takes.  An output may be its
+ *     own input (same pointer, same strides); other overlaps are not allowed.
+ *   - freqs: [rot/2] float64, device (sinkhorn_attn_rotary_freqs); pos: [B][L]
+ *     int32, device, or NULL (token t has position t).
+ *   - k, k_out may be NULL when Hk == 0 (queries alone).
+ */
+typedef struct {
+    int B, Hq, Hk, L, d;       /* d a multiple of 8, at most 256; Hk >= 0 */
+    int rot;                   /* leading channels that are turned, even, 2 <= rot <= d */
+    int interleaved;           /* 0 or 1 */
+    float scale;               /* finite */
+    sa_dtype dtype;
+    long long q_stride[3], k_stride[3], q_out_stride[3], k_out_stride[3];
+} sa_rotary_params;
+
+sa_status sinkhorn_attn_rotary_fwd(const sa_rotary_params* p, const double* freqs, const int* pos,
+                                   const void* q, const void* k, void* q_out, void* k_out,
+                                   void* stream);
+/* dq, dk: the gradients of the outputs; dq_in, dk_in (written): of the inputs. */
+sa_status sinkhorn_attn_rotary_bwd(const sa_rotary_params* p, const double* freqs, const int* pos,
+                                   const void* dq, const void* dk, void* dq_in, void* dk_in,
+                                   void* stream);
+
+/* How the frequencies are stretched for contexts longer than the trained one. */
+typedef enum {
+    SA_ROTARY_PLAIN = 0,     /* base^(-2i/rot) */
+    SA_ROTARY_LINEAR = 1,    /* divided by factor (positions interpolated) */
+    SA_ROTARY_NTK = 2,       /* base replaced by base * factor^(rot / (rot - 2)) */
+    SA_ROTARY_BY_PARTS = 3   /* YaRN: pairs that turn more than turns_hi times over
+                                train_len tokens are kept, fewer than turns_lo divided
+                                by factor, a linear mix in the pair index between */
+} sa_rotary_scaling;
+
+/* Host-only arithmetic (no device work): writes freqs[0 .. rot/2) (host) in
+ * radians per position, and to *scale (may be NULL) the factor on the rotated
+ * channels: 0.1 ln(factor) + 1 for SA_ROTARY_BY_PARTS, else 1.  train_len,
+ * turns_hi and turns_lo are read only by SA_ROTARY_BY_PARTS (usual turns: 32
+ * and 1).  Returns SA_ERR_INVALID_ARG for rot < 2 or odd, base <= 1 or factor
+ * < 1 or not finite, an unknown kind, train_len <= 0, or turns that do not
+ * satisfy turns_hi > turns_lo > 0. */
+sa_status sinkhorn_attn_rotary_freqs(int rot, double base, sa_rotary_scaling kind, double factor,
+                                     double train_len, double turns_hi, double turns_lo,
+                                     double* freqs, float* scale);
+
 /* Test hook for the exponentials of the row-sum sweeps (the dual updates and
  * the vector-cotangent sweeps); no counterpart in the pages.  For each of the
  * n float32 arguments x (x <= 0; device, 4-byte aligned) it writes 2^x as those
