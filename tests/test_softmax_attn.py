@@ -72,7 +72,7 @@ def test_bad_strides_are_refused(which, stride):
 
 def test_workspace_is_bounded_and_grows_with_the_rows_only():
     # single tokens: parts of the rows, within the stated bound whatever the cache
-    for Lk in (128, 4096, 1 << 20, 1 << 30):
+    for Lk in (128, 4096, 1 << 20, 1 << 26):
         for B in (1, 3, 64, 147):
             f, _ = sa.sinkhorn_attn_softmax_workspace_size(P(B=B, Hq=64, Hk=1, Lq=1, Lk=Lk, W=Lk))
             assert f <= 37 << 20
