@@ -89,13 +89,13 @@ __global__ void __launch_bounds__(128) k_join(const Args a) {
         o.x = fmaf(w, y.x, o.x);
         o.y = fmaf(w, y.y, o.y);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN stays one
+    const float inv = m == -INFINITY ? 0.f : 1.f / l;  // no part holds a key: zeros
     const int t = (int)(row % a.Lq);
     const long long bh = row / a.Lq;
     T* out = a.o.at<T>((int)(bh / a.Hq), (int)(bh % a.Hq), t) + 2 * lane;
     store_elem(out, o.x * inv);
     store_elem(out + 1, o.y * inv);
-    if (lane == 0) a.u[row] = l == 0.f ? 0.f : -(m + lg2(l)) * kLn2;
+    if (lane == 0) a.u[row] = m == -INFINITY ? 0.f : -(m + lg2(l)) * kLn2;
 }
 
 }  // namespace sm

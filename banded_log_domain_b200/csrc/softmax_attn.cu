@@ -2,10 +2,12 @@
 // validation, the launch plan and the launches.
 #include <cmath>
 #include <algorithm>
+#include <cstring>
 
 #include "host_util.cuh"
 #include "softmax.cuh"
 #include "softmax_simt.cuh"
+#include "softmax_tc.cuh"
 
 namespace sa {
 namespace {
@@ -13,10 +15,11 @@ namespace {
 constexpr int kD = 64;
 constexpr int kMaxGroup = 64;   // query heads per key head (they share a tile's rows)
 
-// How a call is cut: query tiles of `nq` queries x the group's heads, the
-// forward's keys in `nsplit` parts per tile, each part in `nparts / nsplit`.
+// How a call is cut: tiles of `nq` queries x the group's heads, `per` queries to
+// a forward item, its keys in `nsplit` parts.
 struct Plan {
-    int G, nq, ntile, nktile, nsplit, nparts;
+    bool tc, alt;
+    int G, nq, per, ntile, nktile, nsplit, nparts;
     long long rows;  // B * Hq * Lq
     size_t fwd_bytes, bwd_bytes, part_ml;
 };
@@ -36,23 +39,30 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     // token indices stay clear of 2^31 with a tile's rows added
     if (p->Lk > (1 << 30) || (long long)p->B * p->Hq > 65535) return SA_ERR_UNSUPPORTED;
     pl->rows = (long long)p->B * p->Hq * p->Lq;
-    const int M = 64, N = 64;  // rows of a tile, keys of a chunk
-    pl->nq = M / pl->G;
-    pl->ntile = (p->Lq + pl->nq - 1) / pl->nq;
-    pl->nktile = (p->Lk + 63) / 64;
-    // A few query rows over many keys (single new tokens) would leave most SMs
-    // idle: then every tile's keys are cut into parts for about two blocks an
-    // SM, of at least four chunks each, joined by a second kernel.
-    const long long tiles = (long long)p->B * p->Hk * pl->ntile;
-    if (std::max(tiles, (long long)p->B * p->Hk * pl->nktile) > (1LL << 30)) return SA_ERR_UNSUPPORTED;
+    pl->tc = p->dtype == SA_BF16;
+    const int sms = sm_count(), N = pl->tc ? 128 : 64;  // keys of a chunk
+    pl->nq = (pl->tc ? 128 : 64) / pl->G;
     const long long W = std::min(p->W, p->Lk);
     const long long keys = std::min<long long>(p->Lk, W + (p->causal ? 0 : W) + pl->nq);
     const long long chunks = (keys + N - 1) / N;
+    // The tensor-core forward's items are two sub-tiles of nq queries, or, where
+    // one holds every query and there are several chunks, the same rows twice
+    // (ALT), each taking half of the chunks.
+    const long long BH = (long long)p->B * p->Hk;
+    pl->alt = pl->tc && p->Lq <= pl->nq && chunks >= 4 && BH <= 3LL * sms;
+    pl->per = pl->tc && !pl->alt ? 2 * pl->nq : pl->nq;
+    pl->ntile = (p->Lq + pl->per - 1) / pl->per;
+    pl->nktile = (p->Lk + 63) / 64;
+    const long long tiles = BH * pl->ntile;
+    if (std::max(tiles, BH * pl->nktile) > (1LL << 30)) return SA_ERR_UNSUPPORTED;
+    // A few query rows over many keys (single new tokens) would leave most SMs
+    // idle: then every tile's keys are cut into parts for about two blocks an
+    // SM, of at least four chunks each, joined by a second kernel.
     pl->nsplit = 1;
-    if (tiles > 0 && tiles < sm_count())
-        pl->nsplit = (int)std::max<long long>(1, std::min((2LL * sm_count() + tiles - 1) / tiles, chunks / 4));
-    pl->nparts = pl->nsplit;
-    const long long parts = pl->nsplit > 1 ? pl->rows * pl->nparts : 0;
+    if (tiles > 0 && tiles < sms)
+        pl->nsplit = (int)std::max<long long>(1, std::min(2LL * sms / tiles, chunks / 4));
+    pl->nparts = pl->alt ? 2 * pl->nsplit : pl->nsplit;
+    const long long parts = pl->nparts > 1 ? pl->rows * pl->nparts : 0;
     pl->part_ml = kHeader + align_up((size_t)parts * kD * 4);
     pl->fwd_bytes = pl->part_ml + align_up((size_t)parts * 8);
     pl->bwd_bytes = kHeader + align_up((size_t)pl->rows * 4);
@@ -111,26 +121,61 @@ void base_args(sm::Args* a, const sa_softmax_params* p, const Plan& pl, const ui
     a->exact_d = 0;
 }
 
-template <typename T>
-cudaError_t fwd_launch(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
+cudaError_t fwd_simt(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
     const long long tiles = (long long)p->B * p->Hk * pl.ntile;
-    cudaError_t e = launch(sm::simt::k_fwd<T>, tiles * pl.nsplit, sm::simt::THREADS, sm::simt::smem_bytes(4), st, a);
-    if (e == cudaSuccess && pl.nsplit > 1) e = launch(sm::k_join<T>, (pl.rows + 3) / 4, 128, 0, st, a);
+    return launch(sm::simt::k_fwd<float>, tiles * pl.nsplit, sm::simt::THREADS, sm::simt::smem_bytes(4), st, a);
+}
+
+// A [B][H][L][64] bf16 view as a 4-D tensor; boxes of `tokens` x `heads` rows.
+bool make_map(CUtensorMap* m, const sm::View& v, int B, int H, int L, int tokens, int heads) {
+    auto fn = encode_tiled();
+    if (!fn) return false;
+    cuuint64_t dims[4] = {kD, (cuuint64_t)L, (cuuint64_t)H, (cuuint64_t)B};
+    cuuint64_t strides[3];
+    const int n[3] = {L, H, B};
+    for (int i = 0; i < 3; ++i) strides[i] = n[i] > 1 ? (cuuint64_t)v.s[2 - i] * 2 : kD * 2;
+    cuuint32_t box[4] = {kD, (cuuint32_t)tokens, (cuuint32_t)heads, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.p, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Persistent: one block per SM, each a share of the items.
+cudaError_t fwd_tc(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
+    using namespace sm::tcf::fwd;
+    Maps maps;
+    if (!make_map(&maps.Q, a.q, p->B, p->Hq, p->Lq, pl.nq, pl.G) || !make_map(&maps.K, a.k, p->B, p->Hk, p->Lk, 128, 1) ||
+        !make_map(&maps.V, a.v, p->B, p->Hk, p->Lk, 128, 1))
+        return cudaErrorInvalidValue;
+    const long long items = (long long)p->B * p->Hk * pl.ntile * pl.nsplit;
+    const unsigned grid = (unsigned)std::min<long long>(items, sm_count());
+    auto kern = pl.alt ? tc_fwd<true> : tc_fwd<false>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(THREADS), SMEM, st, a, maps, (int)items);
     return e;
+}
+
+cudaError_t fwd_launch(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
+    const cudaError_t e = pl.tc ? fwd_tc(p, pl, a, st) : fwd_simt(p, pl, a, st);
+    if (e != cudaSuccess || pl.nparts == 1) return e;
+    return launch(pl.tc ? sm::k_join<__nv_bfloat16> : sm::k_join<float>, (pl.rows + 3) / 4, 128, 0, st, a);
 }
 
 template <typename T>
 cudaError_t bwd_launch(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cudaStream_t st) {
-    const long long tiles = (long long)p->B * p->Hk * pl.ntile;
+    const long long BH = (long long)p->B * p->Hk;
+    a.nq = 64 / pl.G;
+    a.ntile = (p->Lq + a.nq - 1) / a.nq;
     if (pl.rows > 0) {
-        const cudaError_t e = launch(sm::simt::k_bwd_q<T>, tiles, sm::simt::THREADS, sm::simt::smem_bytes(5), st, a);
+        const cudaError_t e =
+            launch(sm::simt::k_bwd_q<T>, BH * a.ntile, sm::simt::THREADS, sm::simt::smem_bytes(5), st, a);
         if (e != cudaSuccess) return e;
     } else {
         a.Lq = 0;  // no query: the key sweep writes zeros
     }
     a.ntile = pl.nktile;
-    return launch(sm::simt::k_bwd_kv<T>, (long long)p->B * p->Hk * pl.nktile, sm::simt::THREADS,
-                  sm::simt::smem_bytes(6), st, a);
+    return launch(sm::simt::k_bwd_kv<T>, BH * pl.nktile, sm::simt::THREADS, sm::simt::smem_bytes(6), st, a);
 }
 
 }  // namespace
@@ -171,8 +216,7 @@ sa_status sinkhorn_attn_softmax_fwd(const sa_softmax_params* p, const void* q, c
     a.part_o = (float*)((char*)ws + kHeader);
     a.part_ml = (float2*)((char*)ws + pl.part_ml);
     const cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e =
-        p->dtype == SA_F32 ? fwd_launch<float>(p, pl, a, st) : fwd_launch<__nv_bfloat16>(p, pl, a, st);
+    const cudaError_t e = fwd_launch(p, pl, a, st);
     return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 

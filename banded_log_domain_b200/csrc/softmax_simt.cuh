@@ -225,7 +225,8 @@ __global__ void __launch_bounds__(THREADS) k_fwd(const Args a) {
         if (a.nsplit > 1) {
             const long long at = row * a.nparts + rt.part;
             store4(a.part_o + at * 64 + tx * 4, x[0], x[1], x[2], x[3]);
-            if (tx == 0) a.part_ml[at] = make_float2(m[i], total);
+            // a NaN among the scores stays one when the parts are joined
+            if (tx == 0) a.part_ml[at] = make_float2(total != total && m[i] == -INFINITY ? 0.f : m[i], total);
             continue;
         }
         const float inv = total == 0.f ? 0.f : 1.f / total;  // a NaN stays one
