@@ -15,11 +15,11 @@ namespace {
 constexpr int kD = 64;
 constexpr int kMaxGroup = 64;   // query heads per key head (they share a tile's rows)
 
-// How a call is cut: tiles of `nq` queries x the group's heads, `per` queries to
-// a forward item, its keys in `nsplit` parts.
+// How a call is cut: tiles of `nq` queries x the group's heads, `nr` tiles (`per`
+// queries) to a forward item, its keys in `nsplit` parts.
 struct Plan {
-    bool tc, alt;
-    int G, nq, per, ntile, nktile, nsplit, nparts;
+    bool tc;
+    int G, nq, nr, per, ntile, nktile, nsplit, nparts;
     long long rows;  // B * Hq * Lq
     size_t fwd_bytes, bwd_bytes, part_ml;
 };
@@ -40,28 +40,27 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     if (p->Lk > (1 << 30) || (long long)p->B * p->Hq > 65535) return SA_ERR_UNSUPPORTED;
     pl->rows = (long long)p->B * p->Hq * p->Lq;
     pl->tc = p->dtype == SA_BF16;
-    const int sms = sm_count(), N = pl->tc ? 128 : 64;  // keys of a chunk
+    const int sms = sm_count();
     pl->nq = (pl->tc ? 128 : 64) / pl->G;
-    const long long W = std::min(p->W, p->Lk);
-    const long long keys = std::min<long long>(p->Lk, W + (p->causal ? 0 : W) + pl->nq);
-    const long long chunks = (keys + N - 1) / N;
-    // The tensor-core forward's items are two sub-tiles of nq queries, or, where
-    // one holds every query and there are several chunks, the same rows twice
-    // (ALT), each taking half of the chunks.
-    const long long BH = (long long)p->B * p->Hk;
-    pl->alt = pl->tc && p->Lq <= pl->nq && chunks >= 4 && BH <= 3LL * sms;
-    pl->per = pl->tc && !pl->alt ? 2 * pl->nq : pl->nq;
-    pl->ntile = (p->Lq + pl->per - 1) / pl->per;
+    const long long BH = (long long)p->B * p->Hk, RT = (p->Lq + pl->nq - 1) / pl->nq;  // row tiles
+    // The tensor-core forward's items are 4, 2 or 1 row tiles (see softmax_tc.cuh).
+    pl->nr = 1;
+    if (pl->tc && RT > 1) pl->nr = BH * ((RT + 3) / 4) >= 4LL * sms ? 4 : 2;
+    pl->per = pl->nr * pl->nq;
+    pl->ntile = (int)((RT + pl->nr - 1) / pl->nr);
     pl->nktile = (p->Lk + 63) / 64;
     const long long tiles = BH * pl->ntile;
     if (std::max(tiles, BH * pl->nktile) > (1LL << 30)) return SA_ERR_UNSUPPORTED;
     // A few query rows over many keys (single new tokens) would leave most SMs
     // idle: then every tile's keys are cut into parts for about two blocks an
     // SM, of at least four chunks each, joined by a second kernel.
+    const long long W = std::min(p->W, p->Lk);
+    const long long keys = std::min<long long>(p->Lk, W + (p->causal ? 0 : W) + pl->per);
+    const long long chunks = (keys + 63) / 64;
     pl->nsplit = 1;
     if (tiles > 0 && tiles < sms)
-        pl->nsplit = (int)std::max<long long>(1, std::min(2LL * sms / tiles, chunks / 4));
-    pl->nparts = pl->alt ? 2 * pl->nsplit : pl->nsplit;
+        pl->nsplit = (int)std::max<long long>(1, std::min(2LL * sms / tiles, chunks / (pl->tc ? 8 : 4)));
+    pl->nparts = pl->nsplit;
     const long long parts = pl->nparts > 1 ? pl->rows * pl->nparts : 0;
     pl->part_ml = kHeader + align_up((size_t)parts * kD * 4);
     pl->fwd_bytes = pl->part_ml + align_up((size_t)parts * 8);
@@ -142,22 +141,26 @@ bool make_map(CUtensorMap* m, const sm::View& v, int B, int H, int L, int tokens
 }
 
 // Persistent: one block per SM, each a share of the items.
+template <int NR>
 cudaError_t fwd_tc(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
     using namespace sm::tcf::fwd;
     Maps maps;
-    if (!make_map(&maps.Q, a.q, p->B, p->Hq, p->Lq, pl.nq, pl.G) || !make_map(&maps.K, a.k, p->B, p->Hk, p->Lk, 128, 1) ||
-        !make_map(&maps.V, a.v, p->B, p->Hk, p->Lk, 128, 1))
+    if (!make_map(&maps.Q, a.q, p->B, p->Hq, p->Lq, pl.nq, pl.G) || !make_map(&maps.K, a.k, p->B, p->Hk, p->Lk, 64, 1) ||
+        !make_map(&maps.V, a.v, p->B, p->Hk, p->Lk, 64, 1))
         return cudaErrorInvalidValue;
     const long long items = (long long)p->B * p->Hk * pl.ntile * pl.nsplit;
     const unsigned grid = (unsigned)std::min<long long>(items, sm_count());
-    auto kern = pl.alt ? tc_fwd<true> : tc_fwd<false>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    if (e == cudaSuccess) e = launch_pdl(kern, dim3(grid), dim3(THREADS), SMEM, st, a, maps, (int)items);
+    constexpr int smem = Lay<NR>::SMEM;
+    cudaError_t e = cudaFuncSetAttribute(tc_fwd<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = launch_pdl(tc_fwd<NR>, dim3(grid), dim3(THREADS), smem, st, a, maps, (int)items);
     return e;
 }
 
 cudaError_t fwd_launch(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
-    const cudaError_t e = pl.tc ? fwd_tc(p, pl, a, st) : fwd_simt(p, pl, a, st);
+    const cudaError_t e = !pl.tc       ? fwd_simt(p, pl, a, st)
+                          : pl.nr == 4 ? fwd_tc<4>(p, pl, a, st)
+                          : pl.nr == 2 ? fwd_tc<2>(p, pl, a, st)
+                                       : fwd_tc<1>(p, pl, a, st);
     if (e != cudaSuccess || pl.nparts == 1) return e;
     return launch(pl.tc ? sm::k_join<__nv_bfloat16> : sm::k_join<float>, (pl.rows + 3) / 4, 128, 0, st, a);
 }

@@ -42,10 +42,20 @@ struct Ctl {
     __device__ bool wait_warp(int slot, uint32_t parity) { return __all_sync(~0u, wait(slot, parity)); }
 };
 
-__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+// The largest of three; NaN if any is.
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
     float y;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
+}
+// Registers per thread of the calling warpgroup from here on.
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Items in the order of falling work (a causal band grows with the position),
@@ -94,113 +104,138 @@ __device__ __forceinline__ uint32_t range_bits(int a, int b) {
 }
 
 // ---------------------------------------------------------------------------
-// Forward.  An item is a pair of tiles of 128 packed query rows (sub-tiles 0 and
-// 1) of one key head and a part of their keys, walked in chunks of 128 keys that
-// both sub-tiles share.  Eight softmax warps, four per sub-tile, one row per
-// thread; a loader, a mask warp, and one issuing warp per product:
-//   S_t = Q_t K^T    128 x 128 x 64 into TMEM, read by the rows' threads
-//   O_t += P_t V     128 x 64 x 128, P_t bf16 from TMEM
-// A row's scores leave TMEM at once, so S of the next chunk is formed while the
-// exponentials of this one are taken.  The running maximum is only moved when
-// it has grown by more than 8 (in log2 units): until then probabilities are at
-// most 2^8, which the fp32 sums and bf16's exponent hold without loss, and O
-// needs no rescaling.  The mask warp turns the token mask and the ends of the
-// item's keys into one word per 32 columns, and zeroes the rows of V that no
-// query of the item may read (0 times whatever they hold).
-// ALT (few query rows): both sub-tiles hold the same rows and take the chunks in
-// turn, each its own part.
-
+// Forward.  An item is NR tiles of 128 packed query rows of one key head and a
+// part of their keys, walked in chunks of 64 keys that all tiles share.  Four
+// groups of four softmax warps, one row per thread, each run one softmax: NR row
+// tiles times KS = 4 / NR subsets of the chunks (every KS-th), whose results are
+// joined through TMEM at the item's end.  Beside them a loader, a mask warp,
+// and one issuing warp per product:
+//   S = Q K^T    128 x 64 x 64 into TMEM, read by the rows' threads
+//   O += P V     128 x 64 x 64, P bf16 in TMEM over the S it came from
+// Four chains (S, exponentials, P V) in flight hide each other's latency: the
+// same kernel with two groups on chunks of 128 keys spent half its time in the
+// hand-overs.  The running maximum is only moved when it has grown by more than
+// 8 (in log2 units): until then probabilities are at most 2^8, which the fp32
+// sums and bf16's exponent hold without loss, and O needs no rescaling.  The
+// mask warp turns the token mask and the ends of the item's keys into one word
+// per 32 columns, and zeroes the rows of V that no query of the item may read
+// (0 times whatever they hold).
 namespace fwd {
-constexpr int NST = 4;           // key chunk stages
-constexpr int THREADS = 384;
-constexpr int W_LOAD = 8, W_MASK = 9, W_S = 10, W_PV = 11;
-constexpr int OFF_Q = 0;                       // two buffers of two tiles
-constexpr int OFF_ST = OFF_Q + 4 * TILE;       // stages of K and V
-constexpr int OFF_WORDS = OFF_ST + NST * 2 * TILE;
-constexpr int OFF_BAR = OFF_WORDS + NST * 16;
-enum { B_QFULL = 0, B_QEMPTY = 2, B_FULL = 4, B_READY = B_FULL + NST, B_EMPTY = B_READY + NST,
-       B_SFULL = B_EMPTY + NST, B_SEMPTY = B_SFULL + 2, B_PFULL = B_SEMPTY + 2, B_PVDONE = B_PFULL + 2,
-       B_DRAIN = B_PVDONE + 2, NBAR = B_DRAIN + 1 };
-constexpr int OFF_END = OFF_BAR + NBAR * 8 + 16;
-constexpr int SMEM = OFF_END + 1024;
-static_assert(SMEM <= 227 * 1024, "shared memory");
+constexpr int THREADS = 640;
+constexpr int W_LOAD = 16, W_MASK = 17, W_S = 18, W_PV = 19;
+// registers per thread: the block is launched with 96 x 640 = 61440
+constexpr int REG_SOFTMAX = 104, REG_OTHER = 64;
+static_assert(512 * REG_SOFTMAX + 128 * REG_OTHER <= 61440, "register split");
+constexpr int KT = TILE / 2;  // one 64 x 64 bf16 tile of keys or values
+constexpr int NIT = 4;        // items in flight between the loader and the other warps
+
+// What every role needs of an item; the loader writes it, once per block.
+struct Item {
+    int b, hk, i0, part, c0, c1, jlo, vlo, vhi, pad;  // b < 0: no more items
+    int s0[4], s1[4];                                // chunks of each row tile
+    long long first;
+};
+
+template <int NR>
+struct Lay {
+    static constexpr int KS = 4 / NR;
+    static constexpr int NST = NR == 4 ? 5 : NR == 2 ? 8 : 10;  // key chunk stages
+    static constexpr int Q = 0;                                 // two buffers of NR tiles
+    static constexpr int ST = Q + 2 * NR * TILE;                // stages of K and V
+    static constexpr int ITEM = ST + NST * 2 * KT;
+    static constexpr int ML = ITEM + NIT * (int)sizeof(Item);   // maxima and sums of the joined subsets
+    static constexpr int WORDS = ML + (4 - NR) * 128 * 8;
+    static constexpr int BAR = WORDS + NST * 8;
+    // barriers
+    static constexpr int QFULL = 0, QEMPTY = 2, IFULL = 4, IEMPTY = IFULL + NIT, SFULL = IEMPTY + NIT,
+                         PFULL = SFULL + 4, PVDONE = PFULL + 4, MFULL = PVDONE + 4, MEMPTY = MFULL + NR,
+                         DRAIN = MEMPTY + NR, FULL = DRAIN + 1, READY = FULL + NST, EMPTY = READY + NST,
+                         NBAR = EMPTY + NST;
+    static constexpr int END = BAR + NBAR * 8 + 16;
+    static constexpr int SMEM = END + 1024;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(sizeof(Item) % 16 == 0 && BAR % 8 == 0, "alignment");
+};
 
 struct Maps {
     CUtensorMap Q, K, V;
 };
 
-// What every role derives from an item's number.
-template <bool ALT>
-struct Item {
-    int b, hk, i0, part, c0, c1, jlo, vlo, vhi, s0[2], s1[2];
-    long long first;
-    __device__ Item(const Args& a, int idx) {
-        part = idx % a.nsplit;
-        int x = idx / a.nsplit;
-        const int BH = a.B * a.Hk, qt = a.ntile - 1 - x / BH;
-        x %= BH;
-        hk = x % a.Hk;
-        b = x / a.Hk;
-        first = a.first(b);
-        i0 = qt * (ALT ? a.nq : 2 * a.nq);
-        int lo[2], hi[2];
-        tile_keys(a, first, i0, min(i0 + a.nq, a.Lq) - 1, lo[0], hi[0]);
-        lo[1] = 0;
-        hi[1] = -1;
-        if (!ALT && i0 + a.nq < a.Lq) tile_keys(a, first, i0 + a.nq, min(i0 + 2 * a.nq, a.Lq) - 1, lo[1], hi[1]);
-        vlo = 0;
-        vhi = -1;
+template <int NR>
+__device__ __forceinline__ void make_item(const Args& a, int idx, Item& w) {
+    w.part = idx % a.nsplit;
+    int x = idx / a.nsplit;
+    const int BH = a.B * a.Hk, qt = a.ntile - 1 - x / BH;
+    x %= BH;
+    w.hk = x % a.Hk;
+    w.b = x / a.Hk;
+    w.first = a.first(w.b);
+    w.i0 = qt * NR * a.nq;
+    int lo[NR], hi[NR], vlo = 0, vhi = -1;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-            if (hi[t] >= lo[t]) {
-                vlo = vhi < vlo ? lo[t] : min(vlo, lo[t]);
-                vhi = max(vhi, hi[t]);
-            }
-        const int n = (vhi - vlo + 128) / 128;  // 0 when empty
-        jlo = vlo;
-        c0 = (int)((long long)n * part / a.nsplit);
-        c1 = (int)((long long)n * (part + 1) / a.nsplit);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            s0[t] = c0;
-            s1[t] = ALT ? c1 : c0;
-            if (!ALT && hi[t] >= lo[t]) {
-                s0[t] = max(c0, (lo[t] - jlo) / 128);
-                s1[t] = min(c1, (hi[t] - jlo) / 128 + 1);
-            }
+    for (int t = 0; t < NR; ++t) {
+        const int i = w.i0 + t * a.nq;
+        lo[t] = 0;
+        hi[t] = -1;
+        if (i < a.Lq) tile_keys(a, w.first, i, min(i + a.nq, a.Lq) - 1, lo[t], hi[t]);
+        if (hi[t] >= lo[t]) {
+            vlo = vhi < vlo ? lo[t] : min(vlo, lo[t]);
+            vhi = max(vhi, hi[t]);
         }
     }
-    __device__ __forceinline__ bool uses(int c, int t) const {
-        return ALT ? ((c - c0) & 1) == t : c >= s0[t] && c < s1[t];
+    w.vlo = w.jlo = vlo;
+    w.vhi = vhi;
+    const int n = (vhi - vlo + 64) / 64;  // 0 when empty
+    w.c0 = (int)((long long)n * w.part / a.nsplit);
+    w.c1 = (int)((long long)n * (w.part + 1) / a.nsplit);
+#pragma unroll
+    for (int t = 0; t < NR; ++t) {
+        w.s0[t] = w.s1[t] = w.c0;
+        if (hi[t] >= lo[t]) {
+            w.s0[t] = max(w.c0, (lo[t] - vlo) / 64);
+            w.s1[t] = min(w.c1, (hi[t] - vlo) / 64 + 1);
+        }
     }
-};
+}
 
-template <bool ALT>
+template <int NR>
 __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_constant__ Maps maps, int nitems) {
+    using Y = Lay<NR>;
+    constexpr int KS = Y::KS, NST = Y::NST;
     extern __shared__ uint8_t smraw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smraw + 1023) & ~(uintptr_t)1023);
-    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
-    uint32_t* tbase = reinterpret_cast<uint32_t*>(sm + OFF_BAR + NBAR * 8);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + Y::BAR);
+    uint32_t* tbase = reinterpret_cast<uint32_t*>(sm + Y::BAR + Y::NBAR * 8);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tbase + 1);
-    uint32_t* words = reinterpret_cast<uint32_t*>(sm + OFF_WORDS);
+    uint32_t* words = reinterpret_cast<uint32_t*>(sm + Y::WORDS);
+    Item* items = reinterpret_cast<Item*>(sm + Y::ITEM);
     Ctl ctl{bar, abort_flag, a.status};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(bar + B_QFULL + i, 1);
-            tc::mbar_init(bar + B_QEMPTY + i, 1);
-            tc::mbar_init(bar + B_SFULL + i, 1);
-            tc::mbar_init(bar + B_SEMPTY + i, 4);
-            tc::mbar_init(bar + B_PFULL + i, 4);
-            tc::mbar_init(bar + B_PVDONE + i, 1);
+            tc::mbar_init(bar + Y::QFULL + i, 1);
+            tc::mbar_init(bar + Y::QEMPTY + i, 1);
+        }
+        for (int i = 0; i < NIT; ++i) {
+            tc::mbar_init(bar + Y::IFULL + i, 1);
+            tc::mbar_init(bar + Y::IEMPTY + i, 19);  // every warp but the loader
+        }
+        for (int i = 0; i < 4; ++i) {
+            tc::mbar_init(bar + Y::SFULL + i, 1);
+            tc::mbar_init(bar + Y::PFULL + i, 4);
+            tc::mbar_init(bar + Y::PVDONE + i, 1);
+        }
+        for (int i = 0; i < NR; ++i) {
+            tc::mbar_init(bar + Y::MFULL + i, KS > 1 ? 4 * (KS - 1) : 1);
+            tc::mbar_init(bar + Y::MEMPTY + i, 4);
         }
         for (int s = 0; s < NST; ++s) {
-            tc::mbar_init(bar + B_FULL + s, 1);
-            tc::mbar_init(bar + B_READY + s, 1);
-            tc::mbar_init(bar + B_EMPTY + s, 1);
+            tc::mbar_init(bar + Y::FULL + s, 1);
+            tc::mbar_init(bar + Y::READY + s, 1);
+            tc::mbar_init(bar + Y::EMPTY + s, 1);
         }
-        tc::mbar_init(bar + B_DRAIN, 2);
+        tc::mbar_init(bar + Y::DRAIN, 2);
         *abort_flag = 0;
         tc::fence_mbar_init();
     }
@@ -211,372 +246,461 @@ __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    // TMEM columns: S_t at 128 t, P_t (128 bf16 per row) at 256 + 64 t, O_t at 384 + 64 t
-    const uint32_t tm = *tbase, tS = tm, tP = tm + 256, tO = tm + 384;
+    // TMEM columns of group x = t * KS + ks: S (and P, 64 bf16 per row) at 64 x, O at 256 + 64 x
+    const uint32_t tm = *tbase, tS = tm, tO = tm + 256;
     tc::grid_dep_wait();
     tc::grid_dep_launch();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
 
-    Walk walk(nitems);
-    int idx;
-    if (warp == W_LOAD) {
-        // ------------------------------------------------------------ loader (one lane)
-        if (lane == 0) {
-            int it = 0, gc = 0;
-            bool ok = true;
-            for (; ok && walk.next(idx); ++it) {
-                const Item<ALT> w(a, idx);
-                const int qb = it & 1;
-                if (it >= 2 && !ctl.wait(B_QEMPTY + qb, ((it >> 1) - 1) & 1)) break;
-                const uint32_t qbytes = (uint32_t)(a.nq * a.G) * 128u;
-                tc::mbar_expect_tx(bar + B_QFULL + qb, ALT ? qbytes : 2 * qbytes);
-                for (int t = 0; t < (ALT ? 1 : 2); ++t)
-                    tma_load_4d(sm + OFF_Q + (2 * qb + t) * TILE, &maps.Q, bar + B_QFULL + qb, w.i0 + t * a.nq,
-                                w.hk * a.G, w.b);
-                for (int c = w.c0; c < w.c1; ++c, ++gc) {
-                    const int s = gc % NST;
-                    if (gc >= NST && !ctl.wait(B_EMPTY + s, ((gc / NST) - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* st = sm + OFF_ST + s * 2 * TILE;
-                    tc::mbar_expect_tx(bar + B_FULL + s, 2 * TILE);
-                    tma_load_4d(st, &maps.K, bar + B_FULL + s, w.jlo + 128 * c, w.hk, w.b);
-                    tma_load_4d(st + TILE, &maps.V, bar + B_FULL + s, w.jlo + 128 * c, w.hk, w.b);
-                }
-            }
-            // the last loads have landed before the block ends, whatever the others do
-            for (int x = max(0, it - 2); x < it; ++x) tc::mbar_wait(bar + B_QFULL + (x & 1), (x >> 1) & 1, kWaitBudget);
-            for (int x = max(0, gc - NST); x < gc; ++x)
-                tc::mbar_wait(bar + B_FULL + x % NST, (x / NST) & 1, kWaitBudget);
-        }
+    // An item's slot is read in place and handed back to the loader at the item's
+    // end.  (Nothing of it may be indexed by a runtime value in registers: local
+    // memory would go to L2, as the shared memory leaves no L1 to speak of.)
+    auto begin_item = [&](int it) -> bool {
+        return ctl.wait_warp(Y::IFULL + it % NIT, (it / NIT) & 1) && items[it % NIT].b >= 0;
+    };
+    auto end_item = [&](int it) {
         __syncwarp();
-    } else if (warp == W_MASK) {
-        // ------------------------------------------------------------ mask words, unused rows of V
-        int gc = 0;
-        bool ok = true;
-        for (; ok && walk.next(idx);) {
-            const Item<ALT> w(a, idx);
-            for (int c = w.c0; c < w.c1; ++c, ++gc) {
-                const int s = gc % NST, j0 = w.jlo + 128 * c;
-                uint32_t bits[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int j = j0 + 32 * k + lane;
-                    bits[k] = __ballot_sync(~0u, j >= w.vlo && j <= w.vhi && a.live(w.b, j));
-                }
-                if (!ctl.wait_warp(B_FULL + s, (gc / NST) & 1)) {
-                    ok = false;
-                    break;
-                }
-                if (lane < 4) words[4 * s + lane] = lane == 0 ? bits[0] : lane == 1 ? bits[1] : lane == 2 ? bits[2] : bits[3];
-                if ((bits[0] & bits[1] & bits[2] & bits[3]) != ~0u) {
-                    uint8_t* v = sm + OFF_ST + s * 2 * TILE + TILE;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t off = ~bits[k];
-                        while (off) {  // four rows at a time, eight lanes of 16 bytes each
-                            uint32_t m = off;
-                            for (int x = 0; x < (lane >> 3); ++x) m &= m - 1;
-                            if (m)
-                                *reinterpret_cast<uint4*>(v + (32 * k + __ffs(m) - 1) * 128 + (lane & 7) * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                            for (int x = 0; x < 4; ++x) off &= off - 1;
+        if (lane == 0) tc::mbar_arrive(bar + Y::IEMPTY + it % NIT);
+    };
+
+    if (warp >= 16) {
+        reg_dec<REG_OTHER>();
+        if (warp == W_LOAD) {
+            // -------------------------------------------------------- loader (one lane)
+            if (lane == 0) {
+                Walk walk(nitems);
+                int idx, nq = 0, gc = 0;
+                bool ok = true;
+                for (int it = 0; ok; ++it) {
+                    const int e = it % NIT;
+                    if (it >= NIT && !ctl.wait(Y::IEMPTY + e, ((it / NIT) - 1) & 1)) break;
+                    const bool more = walk.next(idx);
+                    Item& w = items[e];
+                    if (more) make_item<NR>(a, idx, w);
+                    else w.b = -1;
+                    tc::mbar_arrive(bar + Y::IFULL + e);
+                    if (!more) break;
+                    const int qb = nq & 1;
+                    if (nq >= 2 && !ctl.wait(Y::QEMPTY + qb, ((nq >> 1) - 1) & 1)) break;
+                    tc::mbar_expect_tx(bar + Y::QFULL + qb, (uint32_t)(NR * a.nq * a.G) * 128u);
+                    for (int t = 0; t < NR; ++t)
+                        tma_load_4d(sm + Y::Q + (NR * qb + t) * TILE, &maps.Q, bar + Y::QFULL + qb, w.i0 + t * a.nq,
+                                    w.hk * a.G, w.b);
+                    ++nq;
+                    const int jlo = w.jlo, hk = w.hk, b = w.b, c1 = w.c1;
+                    for (int c = w.c0; c < c1; ++c, ++gc) {
+                        const int s = gc % NST;
+                        if (gc >= NST && !ctl.wait(Y::EMPTY + s, ((gc / NST) - 1) & 1)) {
+                            ok = false;
+                            break;
                         }
+                        uint8_t* st = sm + Y::ST + s * 2 * KT;
+                        tc::mbar_expect_tx(bar + Y::FULL + s, 2 * KT);
+                        tma_load_4d(st, &maps.K, bar + Y::FULL + s, jlo + 64 * c, hk, b);
+                        tma_load_4d(st + KT, &maps.V, bar + Y::FULL + s, jlo + 64 * c, hk, b);
                     }
-                    tc::fence_async_smem();
                 }
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bar + B_READY + s);
+                // the last loads have landed before the block ends, whatever the others do
+                for (int x = max(0, nq - 2); x < nq; ++x)
+                    tc::mbar_wait(bar + Y::QFULL + (x & 1), (x >> 1) & 1, kWaitBudget);
+                for (int x = max(0, gc - NST); x < gc; ++x)
+                    tc::mbar_wait(bar + Y::FULL + x % NST, (x / NST) & 1, kWaitBudget);
             }
-        }
-    } else if (warp == W_S) {
-        // ------------------------------------------------------------ S = Q K^T
-        const uint32_t id = tc::idesc_bf16(128, 128, false, false);
-        const uint64_t dQ = tc::sdesc_sw128(tc::smem_u32(sm + OFF_Q), 16, 1024);
-        const uint64_t dK = tc::sdesc_sw128(tc::smem_u32(sm + OFF_ST), 16, 1024);
-        int it = 0, gc = 0, n[2] = {0, 0};
-        bool ok = true;
-        for (; ok && walk.next(idx); ++it) {
-            const Item<ALT> w(a, idx);
-            const int qb = it & 1;
-            if (!ctl.wait_warp(B_QFULL + qb, (it >> 1) & 1)) break;
-            for (int c = w.c0; ok && c < w.c1; ++c, ++gc) {
-                const int s = gc % NST;
-                if (!ctl.wait_warp(B_READY + s, (gc / NST) & 1)) {
-                    ok = false;
-                    break;
-                }
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (!w.uses(c, t)) continue;
-                    if (n[t] >= 1 && !ctl.wait_warp(B_SEMPTY + t, (n[t] - 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    ++n[t];
-                    tc::tc_fence_after();
-                    const uint64_t dA = tc::sdesc_add(dQ, (2 * qb + (ALT ? 0 : t)) * TILE);
-                    const uint64_t dB = tc::sdesc_add(dK, s * 2 * TILE);
-                    if (tc::elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc::mma_bf16(tS + 128 * t, tc::sdesc_add(dA, 32 * k), tc::sdesc_add(dB, 32 * k), id, k > 0);
-                        tc::tc_commit(bar + B_SFULL + t);
-                    }
-                    __syncwarp();
-                }
-            }
-            if (!ok) break;
-            if (tc::elect_one()) tc::tc_commit(bar + B_QEMPTY + qb);
             __syncwarp();
-        }
-        if (tc::elect_one()) tc::tc_commit(bar + B_DRAIN);
-        __syncwarp();
-        tc::mbar_wait(bar + B_DRAIN, 0, kWaitBudget);
-    } else if (warp == W_PV) {
-        // ------------------------------------------------------------ O += P V
-        const uint32_t id = tc::idesc_bf16(128, 64, false, true);
-        const uint64_t dV = tc::sdesc_sw128(tc::smem_u32(sm + OFF_ST + TILE), TILE, 1024);
-        int gc = 0, n[2] = {0, 0};
-        bool ok = true;
-        for (; ok && walk.next(idx);) {
-            const Item<ALT> w(a, idx);
-            bool some[2] = {false, false};
-            for (int c = w.c0; ok && c < w.c1; ++c, ++gc) {
-                const int s = gc % NST;
-                if (!ctl.wait_warp(B_READY + s, (gc / NST) & 1)) {
-                    ok = false;
-                    break;
-                }
+        } else if (warp == W_MASK) {
+            // -------------------------------------------------------- mask words, unused rows of V
+            int gc = 0;
+            bool ok = true;
+            for (int it = 0; ok && begin_item(it); ++it) {
+                const Item& w = items[it % NIT];
+                for (int c = w.c0; c < w.c1; ++c, ++gc) {
+                    const int s = gc % NST, j0 = w.jlo + 64 * c;
+                    uint32_t bits[2];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (!w.uses(c, t)) continue;
-                    if (!ctl.wait_warp(B_PFULL + t, n[t] & 1)) {
+                    for (int k = 0; k < 2; ++k) {
+                        const int j = j0 + 32 * k + lane;
+                        bits[k] = __ballot_sync(~0u, j >= w.vlo && j <= w.vhi && a.live(w.b, j));
+                    }
+                    if (!ctl.wait_warp(Y::FULL + s, (gc / NST) & 1)) {
                         ok = false;
                         break;
                     }
-                    ++n[t];
-                    tc::tc_fence_after();
-                    const uint64_t dB = tc::sdesc_add(dV, s * 2 * TILE);
-                    if (tc::elect_one()) {
+                    if (lane < 2) words[2 * s + lane] = lane ? bits[1] : bits[0];
+                    if ((bits[0] & bits[1]) != ~0u) {
+                        uint8_t* v = sm + Y::ST + s * 2 * KT + KT;
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            tc::mma_bf16_ts(tO + 64 * t, tP + 64 * t + 8 * k, tc::sdesc_add(dB, k * 2048), id,
-                                            (some[t] || k > 0) ? 1u : 0u);
-                        tc::tc_commit(bar + B_PVDONE + t);
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t off = ~bits[k];
+                            while (off) {  // four rows at a time, eight lanes of 16 bytes each
+                                uint32_t m = off;
+                                for (int x = 0; x < (lane >> 3); ++x) m &= m - 1;
+                                if (m)
+                                    *reinterpret_cast<uint4*>(v + (32 * k + __ffs(m) - 1) * 128 + (lane & 7) * 16) =
+                                        make_uint4(0, 0, 0, 0);
+                                for (int x = 0; x < 4; ++x) off &= off - 1;
+                            }
+                        }
+                        tc::fence_async_smem();
                     }
                     __syncwarp();
-                    some[t] = true;
+                    if (lane == 0) tc::mbar_arrive(bar + Y::READY + s);
+                }
+                end_item(it);
+            }
+        } else if (warp == W_S) {
+            // -------------------------------------------------------- S = Q K^T
+            const uint32_t id = tc::idesc_bf16(128, 64, false, false);
+            const uint64_t dQ = tc::sdesc_sw128(tc::smem_u32(sm + Y::Q), 16, 1024);
+            const uint64_t dK = tc::sdesc_sw128(tc::smem_u32(sm + Y::ST), 16, 1024);
+            int gc = 0;
+            uint32_t n = 0, seen = 0;  // phases of the four P V barriers
+            bool ok = true;
+            for (int it = 0; ok && begin_item(it); ++it) {
+                const Item& w = items[it % NIT];
+                const int qb = it & 1, c1 = w.c1;
+                if (!ctl.wait_warp(Y::QFULL + qb, (it >> 1) & 1)) break;
+                for (int c = w.c0; ok && c < c1; ++c, ++gc) {
+                    const int s = gc % NST, ks = c % KS;
+                    if (!ctl.wait_warp(Y::READY + s, (gc / NST) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint64_t dB = tc::sdesc_add(dK, s * 2 * KT);
+#pragma unroll
+                    for (int t = 0; t < NR; ++t) {
+                        if (c < w.s0[t] || c >= w.s1[t]) continue;
+                        const int x = t * KS + ks;
+                        // the P V before has read P, which lies over S
+                        if ((seen >> x) & 1) {
+                            if (!ctl.wait_warp(Y::PVDONE + x, (n >> x) & 1)) {
+                                ok = false;
+                                break;
+                            }
+                            n ^= 1u << x;
+                        }
+                        seen |= 1u << x;
+                        tc::tc_fence_after();
+                        const uint64_t dA = tc::sdesc_add(dQ, (NR * qb + t) * TILE);
+                        if (tc::elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tc::mma_bf16(tS + 64 * x, tc::sdesc_add(dA, 32 * k), tc::sdesc_add(dB, 32 * k), id, k > 0);
+                            tc::tc_commit(bar + Y::SFULL + x);
+                        }
+                        __syncwarp();
+                    }
                 }
                 if (!ok) break;
-                if (tc::elect_one()) tc::tc_commit(bar + B_EMPTY + s);
-                __syncwarp();
+                if (tc::elect_one()) tc::tc_commit(bar + Y::QEMPTY + qb);
+                end_item(it);
             }
-        }
-        if (tc::elect_one()) tc::tc_commit(bar + B_DRAIN);
-        __syncwarp();
-        tc::mbar_wait(bar + B_DRAIN, 0, kWaitBudget);
-    } else {
-        // ------------------------------------------------------------ softmax rows
-        const int t = warp >> 2, qd = warp & 3;
-        const int r = qd * 32 + lane;  // row of the sub-tile
-        const int g = r / a.nq, iq = r % a.nq;
-        const uint32_t lanebase = (uint32_t)(qd * 32) << 16;
-        const uint64_t c2p = tc::pk2(a.c2, a.c2);
-        int gc = 0, n = 0;
-        bool ok = true;
-        for (; ok && walk.next(idx);) {
-            const Item<ALT> w(a, idx);
-            const int i = w.i0 + (ALT ? 0 : t * a.nq) + iq;
-            const bool row = g < a.G && i < a.Lq;
-            int lo = 0, hi = -1;
-            {
-                const long long p = w.first + i;
-                if (row && p >= 0 && p < a.Lk && a.live(w.b, (int)p)) a.keys(p, lo, hi);
-            }
-            const bool dead = __all_sync(~0u, hi < lo);  // no row of this warp attends anything
-            float m = -INFINITY;  // running maximum (log2 units), moved in steps of more than 8
-            uint64_t l2[2] = {0, 0};
-            float l = 0.f;
-            bool some = false;
-            for (int c = w.c0; c < w.c1; ++c, ++gc) {
-                if (!w.uses(c, t)) continue;
-                const int s = gc % NST;
-                if (!ctl.wait_warp(B_READY + s, (gc / NST) & 1) || !ctl.wait_warp(B_SFULL + t, n & 1)) {
-                    ok = false;
-                    break;
-                }
-                tc::tc_fence_after();
-                if (dead) {  // its rows of P and O are never read
-                    // the P barrier's last phase is over once its P V is
-                    if (n > 0 && !ctl.wait_warp(B_PVDONE + t, (n - 1) & 1)) {
+            if (tc::elect_one()) tc::tc_commit(bar + Y::DRAIN);
+            __syncwarp();
+            tc::mbar_wait(bar + Y::DRAIN, 0, kWaitBudget);
+        } else {
+            // -------------------------------------------------------- O += P V
+            const uint32_t id = tc::idesc_bf16(128, 64, false, true);
+            const uint64_t dV = tc::sdesc_sw128(tc::smem_u32(sm + Y::ST + KT), KT, 1024);
+            int gc = 0;
+            uint32_t n = 0;  // phases of the four P barriers
+            bool ok = true;
+            for (int it = 0; ok && begin_item(it); ++it) {
+                const Item& w = items[it % NIT];
+                const int c1 = w.c1;
+                uint32_t some = 0;
+                for (int c = w.c0; ok && c < c1; ++c, ++gc) {
+                    const int s = gc % NST, ks = c % KS;
+                    if (!ctl.wait_warp(Y::READY + s, (gc / NST) & 1)) {
                         ok = false;
                         break;
                     }
-                    if (lane == 0) {
-                        tc::mbar_arrive(bar + B_SEMPTY + t);
-                        tc::mbar_arrive(bar + B_PFULL + t);
+                    const uint64_t dB = tc::sdesc_add(dV, s * 2 * KT);
+#pragma unroll
+                    for (int t = 0; t < NR; ++t) {
+                        if (c < w.s0[t] || c >= w.s1[t]) continue;
+                        const int x = t * KS + ks;
+                        if (!ctl.wait_warp(Y::PFULL + x, (n >> x) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        n ^= 1u << x;
+                        tc::tc_fence_after();
+                        if (tc::elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tc::mma_bf16_ts(tO + 64 * x, tS + 64 * x + 8 * k, tc::sdesc_add(dB, k * 2048), id,
+                                                (((some >> x) & 1) || k > 0) ? 1u : 0u);
+                            tc::tc_commit(bar + Y::PVDONE + x);
+                        }
+                        __syncwarp();
+                        some |= 1u << x;
                     }
-                    ++n;
-                    continue;
+                    if (!ok) break;
+                    if (tc::elect_one()) tc::tc_commit(bar + Y::EMPTY + s);
+                    __syncwarp();
                 }
-                uint32_t sv[4][32];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tc::tmem_ld32(tS + 128 * t + lanebase + 32 * k, sv[k]);
-                const int j0 = w.jlo + 128 * c;
-                uint32_t on[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) on[k] = words[4 * s + k] & range_bits(lo - j0 - 32 * k, hi - j0 - 32 * k);
-                const bool full = __all_sync(~0u, (on[0] & on[1] & on[2] & on[3]) == ~0u);
-                tc::tmem_wait_ld();
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bar + B_SEMPTY + t);
-                if (!full) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (!((on[k] >> j) & 1u)) sv[k][j] = 0xff800000u;  // -inf
+                end_item(it);
+            }
+            if (tc::elect_one()) tc::tc_commit(bar + Y::DRAIN);
+            __syncwarp();
+            tc::mbar_wait(bar + Y::DRAIN, 0, kWaitBudget);
+        }
+    } else {
+        // ------------------------------------------------------------ softmax rows
+        reg_inc<REG_SOFTMAX>();
+        const int x = warp >> 2, qd = warp & 3, t = x / KS, ks = x % KS;
+        const int r = qd * 32 + lane;  // row of the tile
+        const int g = r / a.nq, iq = r % a.nq;
+        const uint32_t lanebase = (uint32_t)(qd * 32) << 16;
+        const uint32_t mS = tS + 64 * x + lanebase, mO = tO + 64 * x + lanebase;
+        const uint64_t c2p = tc::pk2(a.c2, a.c2);
+        float2* mls = reinterpret_cast<float2*>(sm + Y::ML) + (t * (KS - 1)) * 128 + r;
+        int gc = 0, n = 0;
+        bool ok = true, lent = false;  // lent: O is being read by the group that joins
+        for (int it = 0; ok && begin_item(it); ++it) {
+            const Item& w = items[it % NIT];
+            // this row's keys, relative to the item's first chunk
+            int lo = 0, hi = -1;
+            {
+                const int i = w.i0 + t * a.nq + iq;
+                const long long p = w.first + i;
+                if (g < a.G && i < a.Lq && p >= 0 && p < a.Lk && a.live(w.b, (int)p)) {
+                    a.keys(p, lo, hi);
+                    lo -= w.jlo;
+                    hi -= w.jlo;
                 }
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int j = 0; j < 32; j += 2)
-                        top[k] = max_nan(top[k], max_nan(__uint_as_float(sv[k][j]), __uint_as_float(sv[k][j + 1])));
-                const float mx = max_nan(max_nan(top[0], top[1]), max_nan(top[2], top[3])) * a.c2;
-                const bool move = mx > m + 8.f || (m == -INFINITY && mx > -INFINITY);
-                // the last P V has read P and added to O
-                if (n > 0 && !ctl.wait_warp(B_PVDONE + t, (n - 1) & 1)) {
+            }
+            const bool dead = __all_sync(~0u, hi < lo);  // no row of this warp attends anything
+            // keys that every row of the warp attends, masks aside
+            const int wlo = __reduce_max_sync(~0u, lo), whi = __reduce_min_sync(~0u, hi);
+            float m = -INFINITY;  // running maximum (log2 units), moved in steps of more than 8
+            uint64_t l2[2] = {0, 0};
+            bool some = false;
+            const int g0 = gc - w.c0, c1 = w.s1[t];  // chunk c is the block's chunk g0 + c
+            for (int c = w.s0[t] + (ks + 4 - w.s0[t] % KS) % KS; c < c1; c += KS) {
+                const int s = (g0 + c) % NST;
+                if (!ctl.wait_warp(Y::READY + s, ((g0 + c) / NST) & 1) || !ctl.wait_warp(Y::SFULL + x, n & 1)) {
                     ok = false;
                     break;
                 }
-                if (__any_sync(~0u, move)) {
-                    const float f = move ? ex2(m - mx) : 1.f;  // 0 from an empty row
-                    if (move) m = mx;
-                    float x, y;
+                ++n;
+                tc::tc_fence_after();
+                if (!dead) {  // a dead warp's rows of P and O are never read
+                    // Scores are read twice, 32 at a time, first for the maximum: held all
+                    // at once they would not fit the registers of sixteen warps.
+                    const int j0 = 64 * c;
+                    const uint2 wd = *reinterpret_cast<const uint2*>(words + 2 * s);
+                    uint32_t on[2] = {wd.x, wd.y};
+                    const bool full = j0 >= wlo && j0 + 63 <= whi && (wd.x & wd.y) == ~0u;
+                    if (!full) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        tc::upk2(l2[e], x, y);
-                        l2[e] = tc::pk2(x * f, y * f);
+                        for (int k = 0; k < 2; ++k) on[k] &= range_bits(lo - j0 - 32 * k, hi - j0 - 32 * k);
                     }
-                    if (some) {
-                        tc::tc_fence_after();
+                    uint32_t sv[32];
+                    auto load = [&](int k) {
+                        tc::tmem_ld32(mS + 32 * k, sv);
+                        tc::tmem_wait_ld();
+                        if (!full) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            uint32_t o[16];
-                            tc::tmem_ld16(tO + 64 * t + lanebase + 16 * e, o);
-                            tc::tmem_wait_ld();
+                            for (int j = 0; j < 32; ++j)
+                                if (!((on[k] >> j) & 1u)) sv[j] = 0xff800000u;  // -inf
+                        }
+                    };
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                            tc::tmem_st16(tO + 64 * t + lanebase + 16 * e, o);
+                    for (int k = 0; k < 2; ++k) {
+                        load(k);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            float& y = top[(j >> 1) & 3];
+                            y = max_nan(y, __uint_as_float(sv[j]), __uint_as_float(sv[j + 1]));
                         }
                     }
-                }
-                if (!(mx < INFINITY)) {  // NaN or +inf among the scores: so is the row
-                    l2[0] = tc::pk2(NAN, NAN);
-                    if (m == -INFINITY) m = 0.f;
-                }
-                const float use = m == -INFINITY ? 0.f : -m;
-                const uint64_t mp = tc::pk2(use, use);
+                    const float mx = max_nan(max_nan(top[0], top[1], top[2]), top[3], top[3]) * a.c2;
+                    const bool move = mx > m + 8.f || (m == -INFINITY && mx > -INFINITY);
+                    if (__any_sync(~0u, move)) {
+                        const float f = move ? ex2(m - mx) : 1.f;  // 0 from an empty row
+                        if (move) m = mx;
+                        float y, z;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t pw[16];
-                    // a word of 32 columns is in use for all rows, for none, or for some
-                    const bool all = full || __all_sync(~0u, on[k] == ~0u);
-                    if (all) {
+                        for (int e = 0; e < 2; ++e) {
+                            tc::upk2(l2[e], y, z);
+                            l2[e] = tc::pk2(y * f, z * f);
+                        }
+                        if (some) {  // S was issued after the last P V had added to O
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const uint64_t x = tc::fma2(
-                                tc::pk2(__uint_as_float(sv[k][2 * j]), __uint_as_float(sv[k][2 * j + 1])), c2p, mp);
-                            float e0, e1;
-                            if (j % 4 == 3) {
-                                exp2_poly2(x, e0, e1);
-                            } else {
-                                tc::upk2(x, e0, e1);
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t o[16];
+                                tc::tmem_ld16(mO + 16 * e, o);
+                                tc::tmem_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tc::tmem_st16(mO + 16 * e, o);
+                            }
+                        }
+                    }
+                    if (!(mx < INFINITY)) {  // NaN or +inf among the scores: so is the row
+                        l2[0] = tc::pk2(NAN, NAN);
+                        if (!(fabsf(m) < INFINITY)) m = 0.f;
+                    }
+                    const float use = m == -INFINITY ? 0.f : -m;
+                    const uint64_t mp = tc::pk2(use, use);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t pw[16];
+                        load(k);
+                        // a word of 32 columns is in use for all rows, for none, or for some
+                        const bool all = full || __all_sync(~0u, on[k] == ~0u);
+                        if (all) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const uint64_t y = tc::fma2(
+                                    tc::pk2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), c2p, mp);
+                                float e0, e1;
+                                if (j % 4 == 3) {
+                                    exp2_poly2(y, e0, e1);
+                                } else {
+                                    tc::upk2(y, e0, e1);
+                                    e0 = ex2(e0);
+                                    e1 = ex2(e1);
+                                }
+                                l2[j & 1] = tc::add2(l2[j & 1], tc::pk2(e0, e1));
+                                pw[j] = tc::pack_bf16(e0, e1);
+                            }
+                        } else if (__any_sync(~0u, on[k] != 0u)) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const uint64_t y = tc::fma2(
+                                    tc::pk2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), c2p, mp);
+                                float e0, e1;
+                                tc::upk2(y, e0, e1);
                                 e0 = ex2(e0);
                                 e1 = ex2(e1);
+                                l2[j & 1] = tc::add2(l2[j & 1], tc::pk2(e0, e1));
+                                pw[j] = tc::pack_bf16(e0, e1);
                             }
-                            l2[j & 1] = tc::add2(l2[j & 1], tc::pk2(e0, e1));
-                            pw[j] = tc::pack_bf16(e0, e1);
-                        }
-                    } else if (__any_sync(~0u, on[k] != 0u)) {
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const uint64_t x = tc::fma2(
-                                tc::pk2(__uint_as_float(sv[k][2 * j]), __uint_as_float(sv[k][2 * j + 1])), c2p, mp);
-                            float e0, e1;
-                            tc::upk2(x, e0, e1);
-                            e0 = ex2(e0);
-                            e1 = ex2(e1);
-                            l2[j & 1] = tc::add2(l2[j & 1], tc::pk2(e0, e1));
-                            pw[j] = tc::pack_bf16(e0, e1);
+                            for (int j = 0; j < 16; ++j) pw[j] = 0u;
                         }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) pw[j] = 0u;
+                        tc::tmem_st16(mS + 16 * k, pw);
                     }
-                    tc::tmem_st16(tP + 64 * t + lanebase + 16 * k, pw);
+                    tc::tmem_wait_st();
+                    some = true;
                 }
-                tc::tmem_wait_st();
+                // the joining group has read this group's O of the item before
+                if (lent && !ctl.wait_warp(Y::MEMPTY + t, (it - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                lent = false;
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bar + B_PFULL + t);
-                ++n;
-                some = true;
+                if (lane == 0) tc::mbar_arrive(bar + Y::PFULL + x);
             }
             if (!ok) break;
+            gc += w.c1 - w.c0;
+            float l;
             {
                 float x0, x1, x2, x3;
                 tc::upk2(l2[0], x0, x1);
                 tc::upk2(l2[1], x2, x3);
                 l = (x0 + x1) + (x2 + x3);
             }
-            const long long at = ((long long)w.b * a.Hq + w.hk * a.G + g) * a.Lq + i;
-            uint32_t o[2][32];
-            if (some) {  // false where this warp formed no P
-                if (!ctl.wait_warp(B_PVDONE + t, (n - 1) & 1)) break;
-                tc::tc_fence_after();
-                tc::tmem_ld32(tO + 64 * t + lanebase, o[0]);
-                tc::tmem_ld32(tO + 64 * t + lanebase + 32, o[1]);
-                tc::tmem_wait_ld();
+            if (some && !ctl.wait_warp(Y::PVDONE + x, (n - 1) & 1)) break;
+            tc::tc_fence_after();
+            if (KS > 1 && ks > 0) {  // hand O, the maximum and the sum to the group of subset 0
+                if (lent && !ctl.wait_warp(Y::MEMPTY + t, (it - 1) & 1)) break;
+                mls[(ks - 1) * 128] = make_float2(m, l);
                 tc::tc_fence_before();
-            } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) o[0][j] = o[1][j] = 0u;
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bar + Y::MFULL + t);
+                lent = true;
+                end_item(it);
+                continue;
             }
-            if (!row) continue;
-            if (a.nparts > 1) {
-                const long long pa = at * a.nparts + (ALT ? 2 * w.part + t : w.part);
-                a.part_ml[pa] = make_float2(m, l);
-                if (m > -INFINITY) {
-                    float4* po = reinterpret_cast<float4*>(a.part_o + pa * 64);
+            float f = 1.f;                    // weights of the subsets' O
+            float fs[KS > 1 ? KS - 1 : 1];
+            if (KS > 1) {
+                if (!ctl.wait_warp(Y::MFULL + t, it & 1)) break;
+                tc::tc_fence_after();
+                float mm = m, ms[KS > 1 ? KS - 1 : 1], ls[KS > 1 ? KS - 1 : 1];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            po[8 * k + j] = make_float4(__uint_as_float(o[k][4 * j]), __uint_as_float(o[k][4 * j + 1]),
-                                                        __uint_as_float(o[k][4 * j + 2]), __uint_as_float(o[k][4 * j + 3]));
+                for (int e = 0; e < KS - 1; ++e) {
+                    const float2 y = mls[e * 128];
+                    ms[e] = y.x;
+                    ls[e] = y.y;
+                    mm = fmaxf(mm, y.x);
                 }
-            } else {
-                const bool none = m == -INFINITY;  // nothing attended
-                const float inv = none ? 0.f : 1.f / l;
-                uint4* out = reinterpret_cast<uint4*>(a.o.at<__nv_bfloat16>(w.b, w.hk * a.G + g, i));
+                const float use = mm == -INFINITY ? 0.f : mm;
+                f = ex2(m - use);
+                l = m == -INFINITY ? 0.f : l * f;
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+                for (int e = 0; e < KS - 1; ++e) {
+                    fs[e] = ex2(ms[e] - use);
+                    if (ms[e] != -INFINITY) l = fmaf(ls[e], fs[e], l);
+                }
+                m = mm;
+            }
+            const bool none = m == -INFINITY;  // nothing attended
+            const bool parts = a.nparts > 1;
+            const float inv = parts ? 1.f : none ? 0.f : 1.f / l;
+            const int i = w.i0 + t * a.nq + iq;
+            const bool row = g < a.G && i < a.Lq;
+            const long long at = ((long long)w.b * a.Hq + w.hk * a.G + g) * a.Lq + i;
+            const long long pa = at * a.nparts + w.part;
+            if (row) {
+                if (parts) a.part_ml[pa] = make_float2(m, l);
+                else a.u[at] = none ? 0.f : -(m + lg2(l)) * kLn2;
+            }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t x[4];
+            for (int k = 0; k < 4; ++k) {
+                uint32_t o[16];
+                tc::tmem_ld16(mO + 16 * k, o);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    // without a chunk, or for a row that attends none, O holds anything
+                    const float y = f * inv * __uint_as_float(o[j]);
+                    o[j] = some && f > 0.f ? __float_as_uint(y) : 0u;
+                }
+                if (KS > 1) {
+#pragma unroll
+                    for (int e = 0; e < KS - 1; ++e) {
+                        uint32_t o2[16];
+                        tc::tmem_ld16(mO + 64 * (e + 1) + 16 * k, o2);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (fs[e] > 0.f)
+                                o[j] = __float_as_uint(fmaf(fs[e] * inv, __uint_as_float(o2[j]), __uint_as_float(o[j])));
+                    }
+                }
+                if (row && parts && !none) {
+                    float4* po = reinterpret_cast<float4*>(a.part_o + pa * 64 + 16 * k);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        po[j] = make_float4(__uint_as_float(o[4 * j]), __uint_as_float(o[4 * j + 1]),
+                                            __uint_as_float(o[4 * j + 2]), __uint_as_float(o[4 * j + 3]));
+                } else if (row && !parts) {
+                    uint4* out = reinterpret_cast<uint4*>(a.o.at<__nv_bfloat16>(w.b, w.hk * a.G + g, i) + 16 * k);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t y[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            x[e] = tc::pack_bf16(__uint_as_float(o[k][8 * j + 2 * e]) * inv,
-                                                 __uint_as_float(o[k][8 * j + 2 * e + 1]) * inv);
-                        out[4 * k + j] = make_uint4(x[0], x[1], x[2], x[3]);
+                            y[e] = tc::pack_bf16(__uint_as_float(o[8 * j + 2 * e]), __uint_as_float(o[8 * j + 2 * e + 1]));
+                        out[j] = make_uint4(y[0], y[1], y[2], y[3]);
                     }
-                a.u[at] = none ? 0.f : -(m + lg2(l)) * kLn2;
+                }
+                __syncwarp();
             }
+            if (KS > 1) {
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bar + Y::MEMPTY + t);
+            }
+            end_item(it);
         }
     }
     tc::tc_fence_before();
