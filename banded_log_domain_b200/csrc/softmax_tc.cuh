@@ -108,8 +108,8 @@ __device__ __forceinline__ uint32_t range_bits(int a, int b) {
 // part of their keys, walked in chunks of 64 keys that all tiles share.  Four
 // groups of four softmax warps, one row per thread, each run one softmax: NR row
 // tiles times KS = 4 / NR subsets of the chunks (every KS-th), whose results are
-// joined through TMEM at the item's end.  Beside them a loader, a mask warp,
-// and one issuing warp per product:
+// joined through TMEM at the item's end.  Beside them a loader, a mask warp and
+// two warps that issue both products:
 //   S = Q K^T    128 x 64 x 64 into TMEM, read by the rows' threads
 //   O += P V     128 x 64 x 64, P bf16 in TMEM over the S it came from
 // Four chains (S, exponentials, P V) in flight hide each other's latency: the
@@ -122,7 +122,7 @@ __device__ __forceinline__ uint32_t range_bits(int a, int b) {
 // (0 times whatever they hold).
 namespace fwd {
 constexpr int THREADS = 640;
-constexpr int W_LOAD = 16, W_MASK = 17, W_S = 18, W_PV = 19;
+constexpr int W_LOAD = 16, W_MASK = 17, W_MMA = 18;  // 18: groups 0 and 1, 19: groups 2 and 3
 // registers per thread: the block is launched with 96 x 640 = 61440
 constexpr int REG_SOFTMAX = 104, REG_OTHER = 64;
 static_assert(512 * REG_SOFTMAX + 128 * REG_OTHER <= 61440, "register split");
@@ -148,7 +148,7 @@ struct Lay {
     static constexpr int BAR = WORDS + NST * 8;
     // barriers
     static constexpr int QFULL = 0, QEMPTY = 2, IFULL = 4, IEMPTY = IFULL + NIT, SFULL = IEMPTY + NIT,
-                         PFULL = SFULL + 4, PVDONE = PFULL + 4, MFULL = PVDONE + 4, MEMPTY = MFULL + NR,
+                         PFULL = SFULL + 4, OFULL = PFULL + 4, MFULL = OFULL + 4, MEMPTY = MFULL + NR,
                          DRAIN = MEMPTY + NR, FULL = DRAIN + 1, READY = FULL + NST, EMPTY = READY + NST,
                          NBAR = EMPTY + NST;
     static constexpr int END = BAR + NBAR * 8 + 16;
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar + Y::QFULL + i, 1);
-            tc::mbar_init(bar + Y::QEMPTY + i, 1);
+            tc::mbar_init(bar + Y::QEMPTY + i, 2);
         }
         for (int i = 0; i < NIT; ++i) {
             tc::mbar_init(bar + Y::IFULL + i, 1);
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(bar + Y::SFULL + i, 1);
             tc::mbar_init(bar + Y::PFULL + i, 4);
-            tc::mbar_init(bar + Y::PVDONE + i, 1);
+            tc::mbar_init(bar + Y::OFULL + i, 1);
         }
         for (int i = 0; i < NR; ++i) {
             tc::mbar_init(bar + Y::MFULL + i, KS > 1 ? 4 * (KS - 1) : 1);
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_
         for (int s = 0; s < NST; ++s) {
             tc::mbar_init(bar + Y::FULL + s, 1);
             tc::mbar_init(bar + Y::READY + s, 1);
-            tc::mbar_init(bar + Y::EMPTY + s, 1);
+            tc::mbar_init(bar + Y::EMPTY + s, 2);
         }
         tc::mbar_init(bar + Y::DRAIN, 2);
         *abort_flag = 0;
@@ -347,98 +347,78 @@ __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_
                 }
                 end_item(it);
             }
-        } else if (warp == W_S) {
-            // -------------------------------------------------------- S = Q K^T
-            const uint32_t id = tc::idesc_bf16(128, 64, false, false);
+        } else {
+            // -------------------------------------------------------- S = Q K^T, O += P V
+            // One lane issues both of a group, the P V of a chunk directly before the
+            // S of the group's next chunk, which overwrites P: MMAs of one thread
+            // execute in order, so neither waits for the other.  Two warps, as eight
+            // MMAs and their hand-over take one warp longer than the exponentials.
+            const int half = warp - W_MMA;
+            const uint32_t id_s = tc::idesc_bf16(128, 64, false, false);
+            const uint32_t id_o = tc::idesc_bf16(128, 64, false, true);
             const uint64_t dQ = tc::sdesc_sw128(tc::smem_u32(sm + Y::Q), 16, 1024);
             const uint64_t dK = tc::sdesc_sw128(tc::smem_u32(sm + Y::ST), 16, 1024);
-            int gc = 0;
-            uint32_t n = 0, seen = 0;  // phases of the four P V barriers
-            bool ok = true;
-            for (int it = 0; ok && begin_item(it); ++it) {
-                const Item& w = items[it % NIT];
-                const int qb = it & 1, c1 = w.c1;
-                if (!ctl.wait_warp(Y::QFULL + qb, (it >> 1) & 1)) break;
-                for (int c = w.c0; ok && c < c1; ++c, ++gc) {
-                    const int s = gc % NST, ks = c % KS;
-                    if (!ctl.wait_warp(Y::READY + s, (gc / NST) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint64_t dB = tc::sdesc_add(dK, s * 2 * KT);
-#pragma unroll
-                    for (int t = 0; t < NR; ++t) {
-                        if (c < w.s0[t] || c >= w.s1[t]) continue;
-                        const int x = t * KS + ks;
-                        // the P V before has read P, which lies over S
-                        if ((seen >> x) & 1) {
-                            if (!ctl.wait_warp(Y::PVDONE + x, (n >> x) & 1)) {
-                                ok = false;
-                                break;
-                            }
-                            n ^= 1u << x;
-                        }
-                        seen |= 1u << x;
-                        tc::tc_fence_after();
-                        const uint64_t dA = tc::sdesc_add(dQ, (NR * qb + t) * TILE);
-                        if (tc::elect_one()) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                tc::mma_bf16(tS + 64 * x, tc::sdesc_add(dA, 32 * k), tc::sdesc_add(dB, 32 * k), id, k > 0);
-                            tc::tc_commit(bar + Y::SFULL + x);
-                        }
-                        __syncwarp();
-                    }
-                }
-                if (!ok) break;
-                if (tc::elect_one()) tc::tc_commit(bar + Y::QEMPTY + qb);
-                end_item(it);
-            }
-            if (tc::elect_one()) tc::tc_commit(bar + Y::DRAIN);
-            __syncwarp();
-            tc::mbar_wait(bar + Y::DRAIN, 0, kWaitBudget);
-        } else {
-            // -------------------------------------------------------- O += P V
-            const uint32_t id = tc::idesc_bf16(128, 64, false, true);
             const uint64_t dV = tc::sdesc_sw128(tc::smem_u32(sm + Y::ST + KT), KT, 1024);
             int gc = 0;
             uint32_t n = 0;  // phases of the four P barriers
             bool ok = true;
             for (int it = 0; ok && begin_item(it); ++it) {
                 const Item& w = items[it % NIT];
-                const int c1 = w.c1;
-                uint32_t some = 0;
-                for (int c = w.c0; ok && c < c1; ++c, ++gc) {
-                    const int s = gc % NST, ks = c % KS;
-                    if (!ctl.wait_warp(Y::READY + s, (gc / NST) & 1)) {
+                const int qb = it & 1, c0 = w.c0, c1 = w.c1, g0 = gc - c0;
+                int s0[NR], s1[NR];
+#pragma unroll
+                for (int t = 0; t < NR; ++t) {
+                    s0[t] = w.s0[t];
+                    s1[t] = w.s1[t];
+                }
+                if (!ctl.wait_warp(Y::QFULL + qb, it >> 1 & 1)) break;
+                for (int c = c0 - KS; ok && c < c1; ++c) {
+                    const int cn = c + KS, ks = cn % KS;  // the chunk whose S is formed
+                    const int s = (g0 + c + NST) % NST, sn = (g0 + cn) % NST;
+                    if (cn < c1 && !ctl.wait_warp(Y::READY + sn, ((g0 + cn) / NST) & 1)) {
                         ok = false;
                         break;
                     }
-                    const uint64_t dB = tc::sdesc_add(dV, s * 2 * KT);
+                    const uint64_t dBv = tc::sdesc_add(dV, s * 2 * KT), dBk = tc::sdesc_add(dK, sn * 2 * KT);
 #pragma unroll
                     for (int t = 0; t < NR; ++t) {
-                        if (c < w.s0[t] || c >= w.s1[t]) continue;
                         const int x = t * KS + ks;
-                        if (!ctl.wait_warp(Y::PFULL + x, (n >> x) & 1)) {
-                            ok = false;
-                            break;
+                        if ((x >> 1) != half) continue;
+                        const bool pv = c >= s0[t] && c < s1[t], sc = cn >= s0[t] && cn < s1[t];
+                        if (pv) {
+                            if (!ctl.wait_warp(Y::PFULL + x, (n >> x) & 1)) {
+                                ok = false;
+                                break;
+                            }
+                            n ^= 1u << x;
                         }
-                        n ^= 1u << x;
                         tc::tc_fence_after();
                         if (tc::elect_one()) {
+                            if (pv) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                tc::mma_bf16_ts(tO + 64 * x, tS + 64 * x + 8 * k, tc::sdesc_add(dB, k * 2048), id,
-                                                (((some >> x) & 1) || k > 0) ? 1u : 0u);
-                            tc::tc_commit(bar + Y::PVDONE + x);
+                                for (int k = 0; k < 4; ++k)
+                                    tc::mma_bf16_ts(tO + 64 * x, tS + 64 * x + 8 * k, tc::sdesc_add(dBv, k * 2048), id_o,
+                                                    (c - KS >= s0[t] || k > 0) ? 1u : 0u);
+                                if (!sc) tc::tc_commit(bar + Y::OFULL + x);  // the group's last
+                            }
+                            if (sc) {
+                                const uint64_t dA = tc::sdesc_add(dQ, (NR * qb + t) * TILE);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    tc::mma_bf16(tS + 64 * x, tc::sdesc_add(dA, 32 * k), tc::sdesc_add(dBk, 32 * k), id_s,
+                                                 k > 0);
+                                tc::tc_commit(bar + Y::SFULL + x);
+                            }
                         }
                         __syncwarp();
-                        some |= 1u << x;
                     }
                     if (!ok) break;
-                    if (tc::elect_one()) tc::tc_commit(bar + Y::EMPTY + s);
+                    if (c >= c0 && tc::elect_one()) tc::tc_commit(bar + Y::EMPTY + s);
                     __syncwarp();
                 }
+                if (!ok) break;
+                gc += c1 - c0;
+                if (tc::elect_one()) tc::tc_commit(bar + Y::QEMPTY + qb);
                 end_item(it);
             }
             if (tc::elect_one()) tc::tc_commit(bar + Y::DRAIN);
@@ -455,7 +435,8 @@ __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_
         const uint32_t mS = tS + 64 * x + lanebase, mO = tO + 64 * x + lanebase;
         const uint64_t c2p = tc::pk2(a.c2, a.c2);
         float2* mls = reinterpret_cast<float2*>(sm + Y::ML) + (t * (KS - 1)) * 128 + r;
-        int gc = 0, n = 0;
+        int gc = 0;
+        uint32_t n = 0, no = 0;  // chunks, and items with any
         bool ok = true, lent = false;  // lent: O is being read by the group that joins
         for (int it = 0; ok && begin_item(it); ++it) {
             const Item& w = items[it % NIT];
@@ -475,23 +456,30 @@ __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_
             const int wlo = __reduce_max_sync(~0u, lo), whi = __reduce_min_sync(~0u, hi);
             float m = -INFINITY;  // running maximum (log2 units), moved in steps of more than 8
             uint64_t l2[2] = {0, 0};
-            bool some = false;
+            bool some = false, used = false;
             const int g0 = gc - w.c0, c1 = w.s1[t];  // chunk c is the block's chunk g0 + c
             for (int c = w.s0[t] + (ks + 4 - w.s0[t] % KS) % KS; c < c1; c += KS) {
                 const int s = (g0 + c) % NST;
-                if (!ctl.wait_warp(Y::READY + s, ((g0 + c) / NST) & 1) || !ctl.wait_warp(Y::SFULL + x, n & 1)) {
+                // (the words are written for a mask alone)
+                if ((a.mask && !ctl.wait_warp(Y::READY + s, ((g0 + c) / NST) & 1)) ||
+                    !ctl.wait_warp(Y::SFULL + x, n & 1)) {
                     ok = false;
                     break;
                 }
                 ++n;
+                used = true;
                 tc::tc_fence_after();
                 if (!dead) {  // a dead warp's rows of P and O are never read
                     // Scores are read twice, 32 at a time, first for the maximum: held all
                     // at once they would not fit the registers of sixteen warps.
                     const int j0 = 64 * c;
-                    const uint2 wd = *reinterpret_cast<const uint2*>(words + 2 * s);
-                    uint32_t on[2] = {wd.x, wd.y};
-                    const bool full = j0 >= wlo && j0 + 63 <= whi && (wd.x & wd.y) == ~0u;
+                    uint32_t on[2] = {~0u, ~0u};
+                    if (a.mask) {
+                        const uint2 wd = *reinterpret_cast<const uint2*>(words + 2 * s);
+                        on[0] = wd.x;
+                        on[1] = wd.y;
+                    }
+                    const bool full = j0 >= wlo && j0 + 63 <= whi && (on[0] & on[1]) == ~0u;
                     if (!full) {
 #pragma unroll
                         for (int k = 0; k < 2; ++k) on[k] &= range_bits(lo - j0 - 32 * k, hi - j0 - 32 * k);
@@ -527,7 +515,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_
                             tc::upk2(l2[e], y, z);
                             l2[e] = tc::pk2(y * f, z * f);
                         }
-                        if (some) {  // S was issued after the last P V had added to O
+                        if (some) {  // the last P V was issued before this S: it has added to O
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 uint32_t o[16];
@@ -607,7 +595,10 @@ __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_
                 tc::upk2(l2[1], x2, x3);
                 l = (x0 + x1) + (x2 + x3);
             }
-            if (some && !ctl.wait_warp(Y::PVDONE + x, (n - 1) & 1)) break;
+            if (used) {
+                if (!ctl.wait_warp(Y::OFULL + x, no & 1)) break;
+                ++no;
+            }
             tc::tc_fence_after();
             if (KS > 1 && ks > 0) {  // hand O, the maximum and the sum to the group of subset 0
                 if (lent && !ctl.wait_warp(Y::MEMPTY + t, (it - 1) & 1)) break;
