@@ -98,5 +98,20 @@ __global__ void __launch_bounds__(128) k_join(const Args a) {
     if (lane == 0) a.u[row] = m == -INFINITY ? 0.f : -(m + lg2(l)) * kLn2;
 }
 
+// dK = dV = 0, one warp per key.
+template <typename T>
+__global__ void __launch_bounds__(128) k_zero(const Args a) {
+    const long long key = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+    if (key >= (long long)a.B * a.Hk * a.Lk) return;
+    const int j = (int)(key % a.Lk), lane = threadIdx.x & 31;
+    const long long bh = key / a.Lk;
+    for (const View* x : {&a.dk, &a.dv}) {
+        T* out = x->at<T>((int)(bh / a.Hk), (int)(bh % a.Hk), j) + 2 * lane;
+        store_elem(out, 0.f);
+        store_elem(out + 1, 0.f);
+    }
+}
+
 }  // namespace sm
 }  // namespace sa

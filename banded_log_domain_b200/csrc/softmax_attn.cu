@@ -8,6 +8,7 @@
 #include "softmax.cuh"
 #include "softmax_simt.cuh"
 #include "softmax_tc.cuh"
+#include "softmax_tc_bwd.cuh"
 
 namespace sa {
 namespace {
@@ -165,20 +166,51 @@ cudaError_t fwd_launch(const sa_softmax_params* p, const Plan& pl, const sm::Arg
     return launch(pl.tc ? sm::k_join<__nv_bfloat16> : sm::k_join<float>, (pl.rows + 3) / 4, 128, 0, st, a);
 }
 
-template <typename T>
-cudaError_t bwd_launch(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cudaStream_t st) {
+cudaError_t bwd_simt(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cudaStream_t st) {
     const long long BH = (long long)p->B * p->Hk;
     a.nq = 64 / pl.G;
     a.ntile = (p->Lq + a.nq - 1) / a.nq;
     if (pl.rows > 0) {
         const cudaError_t e =
-            launch(sm::simt::k_bwd_q<T>, BH * a.ntile, sm::simt::THREADS, sm::simt::smem_bytes(5), st, a);
+            launch(sm::simt::k_bwd_q<float>, BH * a.ntile, sm::simt::THREADS, sm::simt::smem_bytes(5), st, a);
         if (e != cudaSuccess) return e;
-    } else {
-        a.Lq = 0;  // no query: the key sweep writes zeros
     }
     a.ntile = pl.nktile;
-    return launch(sm::simt::k_bwd_kv<T>, BH * pl.nktile, sm::simt::THREADS, sm::simt::smem_bytes(6), st, a);
+    return launch(sm::simt::k_bwd_kv<float>, BH * pl.nktile, sm::simt::THREADS, sm::simt::smem_bytes(6), st, a);
+}
+
+template <int MODE>
+cudaError_t bwd_tc(const sa_softmax_params* p, const sm::Args& a, long long items, cudaStream_t st) {
+    using namespace sm::tcf::bwd;
+    Maps maps;
+    bool ok = true;
+    if (MODE == DQ)
+        ok = make_map(&maps.R1, a.q, p->B, p->Hq, p->Lq, a.nq, a.G) && make_map(&maps.R2, a.dO, p->B, p->Hq, p->Lq, a.nq, a.G) &&
+             make_map(&maps.C1, a.k, p->B, p->Hk, p->Lk, 64, 1) && make_map(&maps.C2, a.v, p->B, p->Hk, p->Lk, 64, 1);
+    else
+        ok = make_map(&maps.R1, a.k, p->B, p->Hk, p->Lk, 128, 1) && make_map(&maps.R2, a.v, p->B, p->Hk, p->Lk, 128, 1) &&
+             make_map(&maps.C1, a.q, p->B, p->Hq, p->Lq, 64, 1) && make_map(&maps.C2, a.dO, p->B, p->Hq, p->Lq, 64, 1);
+    if (!ok) return cudaErrorInvalidValue;
+    const unsigned grid = (unsigned)std::min<long long>(items, sm_count());
+    cudaError_t e = cudaFuncSetAttribute(tc_bwd<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e == cudaSuccess) e = launch_pdl(tc_bwd<MODE>, dim3(grid), dim3(THREADS), SMEM, st, a, maps, (int)items);
+    return e;
+}
+
+// No query: the keys' gradients are zeros.
+cudaError_t zero_grads(const sa_softmax_params* p, sm::Args& a, cudaStream_t st) {
+    const long long n = (long long)p->B * p->Hk * p->Lk;
+    if (p->dtype == SA_F32) return launch(sm::k_zero<float>, (n + 3) / 4, 128, 0, st, a);
+    return launch(sm::k_zero<__nv_bfloat16>, (n + 3) / 4, 128, 0, st, a);
+}
+
+cudaError_t bwd_launch(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cudaStream_t st) {
+    if (!pl.tc) return bwd_simt(p, pl, a, st);
+    const long long BH = (long long)p->B * p->Hk;
+    a.nq = pl.nq;
+    a.ntile = (p->Lq + a.nq - 1) / a.nq;
+    const cudaError_t e = bwd_tc<sm::tcf::bwd::DQ>(p, a, BH * a.ntile, st);
+    return e != cudaSuccess ? e : bwd_tc<sm::tcf::bwd::DKV>(p, a, BH * ((p->Lk + 127) / 128), st);
 }
 
 }  // namespace
@@ -255,8 +287,7 @@ sa_status sinkhorn_attn_softmax_bwd(const sa_softmax_params* p, const void* q, c
     // 64 keys the sweep forms D itself, in a pass of its own over them.
     a.exact_d = p->dtype == SA_BF16 && (long long)a.W + a.R + 1 <= 64;
     const cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e =
-        p->dtype == SA_F32 ? bwd_launch<float>(p, pl, a, st) : bwd_launch<__nv_bfloat16>(p, pl, a, st);
+    const cudaError_t e = pl.rows > 0 ? bwd_launch(p, pl, a, st) : zero_grads(p, a, st);
     return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 

@@ -1,0 +1,624 @@
+// The softmax attention's backward for bf16 storage on the tensor cores.
+//
+// Two sweeps, so that every gradient is summed in one place and in one order:
+//   DQ    rows: 128 packed query rows;  chunks: 64 keys
+//         S = Q K^T, G = dO V^T, dS = P (G - D),  dQ += dS K
+//   DKV   rows: 128 keys;  chunks: 64 queries of one head after another
+//         S^T = K Q^T, G^T = V dO^T,  dV += P^T dO,  dK += dS^T Q
+// with P = 2^(c2 S + u2).  (One sweep that also added into dQ would save two of
+// the seven products but needs atomics, whose order changes results.)
+//
+// A unit is one row tile times one chunk.  S and G of a unit go to one of three
+// slots of TMEM; a team of eight warps (two per lane quadrant, 32 columns each)
+// reads them, forms P and dS and writes them as bf16 over the S and G they came
+// from, from where the second products read them as their A operand.  Two teams
+// take the units in turn.  One warp issues S and G, another the second products
+// (one thread for all that add into an accumulator); a loader brings the tiles,
+// and an aux warp prepares each item's rows (D = dO . O among them) and each
+// chunk's columns (mask words; u and D of queries; zeroed operand rows of tokens
+// that are not in use, as 0 times what they hold need not be 0).
+#pragma once
+
+#include "softmax_tc.cuh"
+
+namespace sa {
+namespace sm {
+namespace tcf {
+namespace bwd {
+
+enum { DQ = 0, DKV = 1 };
+constexpr int THREADS = 640;
+constexpr int W_LOAD = 16, W_AUX = 17, W_SG = 18, W_AC = 19;
+constexpr int REG_TEAM = 104, REG_OTHER = 64;  // launched with 96 x 640 = 61440
+static_assert(512 * REG_TEAM + 128 * REG_OTHER <= 61440, "register split");
+constexpr int KT = TILE / 2;
+constexpr int NST = 8, NIT = 4, NSLOT = 3;
+
+struct Item {
+    int b, hk, r0, n, c0, vlo, vhi, pad;  // b < 0: no more; r0: first query or key; c0: column of chunk 0
+    // columns vlo .. vhi (absolute) are in some row's band; n chunks per head
+    long long first;
+};
+struct Row {
+    float u2, D;
+    int lo, hi;  // columns in the band, relative to c0
+};
+
+constexpr int OFF_R = 0;                        // two buffers of two row tiles
+constexpr int OFF_ST = OFF_R + 4 * TILE;        // stages of two chunk tiles
+constexpr int OFF_ITEM = OFF_ST + NST * 2 * KT;
+constexpr int OFF_ROW = OFF_ITEM + NIT * (int)sizeof(Item);
+constexpr int OFF_COL = OFF_ROW + 2 * 128 * (int)sizeof(Row);  // per stage: u2[64], D[64]
+constexpr int OFF_XD = OFF_COL + NST * 512;     // two buffers of shares of D, [4][128]
+constexpr int OFF_WORDS = OFF_XD + 4096;
+constexpr int OFF_BAR = OFF_WORDS + NST * 8;
+enum { RFULL = 0, REMPTY = 2, IFULL = 4, IEMPTY = IFULL + NIT, ROWFULL = IEMPTY + NIT, ROWEMPTY = ROWFULL + 2,
+       SGFULL = ROWEMPTY + 2, DSFULL = SGFULL + NSLOT, SLOT = DSFULL + NSLOT, ACCFULL = SLOT + NSLOT,
+       ACCEMPTY = ACCFULL + 2, XDSUM = ACCEMPTY + 2, DRAIN = XDSUM + 1, FULL = DRAIN + 1, READY = FULL + NST,
+       EMPTY = READY + NST, NBAR = EMPTY + NST };
+constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
+static_assert(SMEM <= 227 * 1024, "shared memory");
+static_assert(sizeof(Item) % 8 == 0 && OFF_ROW % 16 == 0 && OFF_COL % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
+
+struct Maps {
+    CUtensorMap R1, R2, C1, C2;  // DQ: Q, dO, K, V;  DKV: K, V, Q, dO
+};
+
+template <int MODE>
+__device__ __forceinline__ void make_item(const Args& a, int idx, Item& w) {
+    const int BH = a.B * a.Hk, x = idx % BH, rt = idx / BH;
+    w.hk = x % a.Hk;
+    w.b = x / a.Hk;
+    w.first = a.first(w.b);
+    int lo = 0, hi = -1;
+    if (MODE == DQ) {  // the later the query, the more keys a causal band holds
+        w.r0 = (a.ntile - 1 - rt) * a.nq;
+        tile_keys(a, w.first, w.r0, min(w.r0 + a.nq, a.Lq) - 1, lo, hi);
+    } else {  // queries whose position lies in [r0 - R, r0 + 127 + W], and in the sequence
+        w.r0 = rt * 128;
+        long long p0 = (long long)w.r0 - a.R, p1 = (long long)min(w.r0 + 127, a.Lk - 1) + a.W;
+        p0 = p0 > 0 ? p0 : 0;
+        p1 = p1 < a.Lk - 1 ? p1 : a.Lk - 1;
+        p0 -= w.first;
+        p1 -= w.first;
+        if (p0 < 0) p0 = 0;
+        if (p1 > a.Lq - 1) p1 = a.Lq - 1;
+        if (p0 <= p1) {
+            lo = (int)p0;
+            hi = (int)p1;
+        }
+    }
+    w.c0 = w.vlo = lo;
+    w.vhi = hi;
+    w.n = (hi - lo + 64) / 64;  // 0 when empty
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_constant__ Maps maps, int nitems) {
+    extern __shared__ uint8_t smraw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smraw + 1023) & ~(uintptr_t)1023);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(sm + OFF_BAR);
+    uint32_t* tbase = reinterpret_cast<uint32_t*>(sm + OFF_BAR + NBAR * 8);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tbase + 1);
+    uint32_t* words = reinterpret_cast<uint32_t*>(sm + OFF_WORDS);
+    Item* items = reinterpret_cast<Item*>(sm + OFF_ITEM);
+    Row* rows = reinterpret_cast<Row*>(sm + OFF_ROW);
+    float* cols = reinterpret_cast<float*>(sm + OFF_COL);
+    float* xd = reinterpret_cast<float*>(sm + OFF_XD);
+    Ctl ctl{bar, abort_flag, a.status};
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int NACC = MODE == DQ ? 2 : 1;  // accumulator buffers (DQ: of 64 columns; DKV: of 128)
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(bar + RFULL + i, 1);
+            tc::mbar_init(bar + REMPTY + i, 2);
+            tc::mbar_init(bar + ROWFULL + i, 1);
+            tc::mbar_init(bar + ROWEMPTY + i, 16);
+            tc::mbar_init(bar + ACCFULL + i, 1);
+            tc::mbar_init(bar + ACCEMPTY + i, 16);
+        }
+        for (int i = 0; i < NIT; ++i) {
+            tc::mbar_init(bar + IFULL + i, 1);
+            tc::mbar_init(bar + IEMPTY + i, 19);  // every warp but the loader
+        }
+        for (int i = 0; i < NSLOT; ++i) {
+            tc::mbar_init(bar + SGFULL + i, 1);
+            tc::mbar_init(bar + DSFULL + i, 8);
+            tc::mbar_init(bar + SLOT + i, 1);
+        }
+        for (int s = 0; s < NST; ++s) {
+            tc::mbar_init(bar + FULL + s, 1);
+            tc::mbar_init(bar + READY + s, 1);
+            tc::mbar_init(bar + EMPTY + s, 1);
+        }
+        tc::mbar_init(bar + XDSUM, 16);
+        tc::mbar_init(bar + DRAIN, 2);
+        *abort_flag = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 0) {
+        tc::tmem_alloc(tbase, 512);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    // TMEM columns: slot x: S at 128 x, G at 128 x + 64; accumulators from 384
+    const uint32_t tm = *tbase, tA = tm + 384;
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
+    if (MODE == DQ && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
+
+    auto begin_item = [&](int it) -> bool {
+        return ctl.wait_warp(IFULL + it % NIT, (it / NIT) & 1) && items[it % NIT].b >= 0;
+    };
+    auto end_item = [&](int it) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar + IEMPTY + it % NIT);
+    };
+    // units of an item: its chunks, for each head of the group (DKV), or twice (DQ
+    // with exact_d: first D = sum_j P G, then the gradient)
+    const int passes = MODE == DKV ? a.G : a.exact_d ? 2 : 1;
+
+    if (warp >= 16) {
+        reg_dec<REG_OTHER>();
+        if (warp == W_LOAD) {
+            // -------------------------------------------------------- loader (one lane)
+            if (lane == 0) {
+                Walk walk(nitems);
+                int idx, nr = 0, gu = 0;
+                bool ok = true;
+                for (int it = 0; ok; ++it) {
+                    const int e = it % NIT;
+                    if (it >= NIT && !ctl.wait(IEMPTY + e, ((it / NIT) - 1) & 1)) break;
+                    const bool more = walk.next(idx);
+                    Item& w = items[e];
+                    if (more) make_item<MODE>(a, idx, w);
+                    else w.b = -1;
+                    tc::mbar_arrive(bar + IFULL + e);
+                    if (!more) break;
+                    const int rb = nr & 1, n = w.n, hk = w.hk, b = w.b, c0 = w.c0, r0 = w.r0;
+                    if (nr >= 2 && !ctl.wait(REMPTY + rb, ((nr >> 1) - 1) & 1)) break;
+                    const int h0 = MODE == DQ ? hk * a.G : hk;
+                    tc::mbar_expect_tx(bar + RFULL + rb, MODE == DQ ? (uint32_t)(2 * a.nq * a.G) * 128u : 2u * TILE);
+                    tma_load_4d(sm + OFF_R + 2 * rb * TILE, &maps.R1, bar + RFULL + rb, r0, h0, b);
+                    tma_load_4d(sm + OFF_R + (2 * rb + 1) * TILE, &maps.R2, bar + RFULL + rb, r0, h0, b);
+                    ++nr;
+                    for (int p = 0; ok && p < passes; ++p) {
+                        const int h = MODE == DQ ? hk : hk * a.G + p;
+                        for (int c = 0; c < n; ++c, ++gu) {
+                            const int s = gu % NST;
+                            if (gu >= NST && !ctl.wait(EMPTY + s, ((gu / NST) - 1) & 1)) {
+                                ok = false;
+                                break;
+                            }
+                            uint8_t* st = sm + OFF_ST + s * 2 * KT;
+                            tc::mbar_expect_tx(bar + FULL + s, 2 * KT);
+                            tma_load_4d(st, &maps.C1, bar + FULL + s, c0 + 64 * c, h, b);
+                            tma_load_4d(st + KT, &maps.C2, bar + FULL + s, c0 + 64 * c, h, b);
+                        }
+                    }
+                }
+                // the last loads have landed before the block ends, whatever the others do
+                for (int x = max(0, nr - 2); x < nr; ++x)
+                    tc::mbar_wait(bar + RFULL + (x & 1), (x >> 1) & 1, kWaitBudget);
+                for (int x = max(0, gu - NST); x < gu; ++x)
+                    tc::mbar_wait(bar + FULL + x % NST, (x / NST) & 1, kWaitBudget);
+            }
+            __syncwarp();
+        } else if (warp == W_AUX) {
+            // -------------------------------------------------------- rows and columns
+            int gu = 0;
+            bool ok = true;
+            for (int it = 0; ok && begin_item(it); ++it) {
+                const Item& w = items[it % NIT];
+                const int rb = it & 1, b = w.b, hk = w.hk, n = w.n, c0 = w.c0;
+                const long long first = w.first;
+                if (it >= 2 && !ctl.wait_warp(ROWEMPTY + rb, ((it >> 1) - 1) & 1)) break;
+                if (!ctl.wait_warp(RFULL + rb, (it >> 1) & 1)) break;
+                Row* row = rows + rb * 128;
+                if (MODE == DQ) {
+                    const uint8_t* g = sm + OFF_R + (2 * rb + 1) * TILE;
+#pragma unroll 1
+                    for (int r0 = 0; r0 < 128; r0 += 16) {  // four rows at a time, eight lanes each
+                        uint4 o[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = r0 + 4 * e + (lane >> 3), t = w.r0 + r % a.nq;
+                            o[e] = make_uint4(0, 0, 0, 0);
+                            if (!a.exact_d && r / a.nq < a.G && t < a.Lq)
+                                o[e] = *reinterpret_cast<const uint4*>(
+                                    a.o.at<__nv_bfloat16>(b, hk * a.G + r / a.nq, t) + 8 * (lane & 7));
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = r0 + 4 * e + (lane >> 3), t = w.r0 + r % a.nq, gh = r / a.nq;
+                            const uint4 y = *reinterpret_cast<const uint4*>(g + tc::sw128_off(r, lane & 7));
+                            const __nv_bfloat162* po = reinterpret_cast<const __nv_bfloat162*>(&o[e]);
+                            const __nv_bfloat162* py = reinterpret_cast<const __nv_bfloat162*>(&y);
+                            float dot = 0.f;
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) {
+                                const float2 f = __bfloat1622float2(po[z]), k = __bfloat1622float2(py[z]);
+                                dot = fmaf(f.x, k.x, fmaf(f.y, k.y, dot));
+                            }
+#pragma unroll
+                            for (int z = 4; z; z >>= 1) dot += __shfl_xor_sync(~0u, dot, z);
+                            if ((lane & 7) == 0) {
+                                Row x;
+                                x.u2 = x.D = 0.f;
+                                x.lo = 0;
+                                x.hi = -1;
+                                if (gh < a.G && t < a.Lq) {
+                                    const long long at = ((long long)b * a.Hq + hk * a.G + gh) * a.Lq + t;
+                                    const long long p = first + t;
+                                    if (p >= 0 && p < a.Lk && a.live(b, (int)p)) {
+                                        a.keys(p, x.lo, x.hi);
+                                        x.lo -= c0;
+                                        x.hi -= c0;
+                                        x.u2 = a.u[at] * kLog2e;
+                                        x.D = dot;
+                                    }
+                                    if (!a.exact_d) a.D[at] = x.D;
+                                }
+                                row[r] = x;
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = 32 * e + lane, j = w.r0 + r;
+                        Row x;
+                        x.u2 = x.D = 0.f;
+                        x.lo = 0;
+                        x.hi = -1;
+                        if (j < a.Lk && a.live(b, j)) {
+                            // queries j - R .. j + W, as columns; the words end them at the last query
+                            const long long lo = (long long)j - a.R - first - c0, hi = (long long)j + a.W - first - c0;
+                            x.lo = (int)(lo < 0 ? 0 : lo > (1 << 30) ? (1 << 30) : lo);
+                            x.hi = (int)(hi < -1 ? -1 : hi > (1 << 30) ? (1 << 30) : hi);
+                        }
+                        row[r] = x;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    tc::mbar_arrive(bar + ROWFULL + rb);
+                    tc::mbar_arrive(bar + REMPTY + rb);
+                }
+                // the columns of a chunk: this lane's two
+                uint32_t bits[2];
+                float cu[2], cD[2];
+                auto fetch = [&](int p, int c) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int j = c0 + 64 * c + 32 * k + lane;
+                        bool on = j >= w.vlo && j <= w.vhi;
+                        cu[k] = cD[k] = 0.f;
+                        if (MODE == DQ) {
+                            on = on && a.live(b, j);
+                        } else {
+                            on = on && a.live(b, (int)(first + j));
+                            if (on) {
+                                const long long at = ((long long)b * a.Hq + hk * a.G + p) * a.Lq + j;
+                                cu[k] = a.u[at] * kLog2e;
+                                cD[k] = a.D[at];
+                            }
+                        }
+                        bits[k] = __ballot_sync(~0u, on);
+                    }
+                };
+                if (n > 0) fetch(0, 0);
+                for (int p = 0; ok && p < passes; ++p) {
+                    for (int c = 0; c < n; ++c, ++gu) {
+                        const int s = gu % NST;
+                        if (!ctl.wait_warp(FULL + s, (gu / NST) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane < 2) words[2 * s + lane] = lane ? bits[1] : bits[0];
+                        if (MODE == DKV) {
+                            float* cv = cols + s * 128;
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                cv[32 * k + lane] = cu[k];
+                                cv[64 + 32 * k + lane] = cD[k];
+                            }
+                        }
+                        if ((bits[0] & bits[1]) != ~0u) {
+                            uint8_t* x = sm + OFF_ST + s * 2 * KT;
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                uint32_t off = ~bits[k];
+                                while (off) {  // four rows at a time, eight lanes of 16 bytes each
+                                    uint32_t m = off;
+                                    for (int z = 0; z < (lane >> 3); ++z) m &= m - 1;
+                                    if (m) {
+                                        uint4* q = reinterpret_cast<uint4*>(x + (32 * k + __ffs(m) - 1) * 128 + (lane & 7) * 16);
+                                        q[0] = make_uint4(0, 0, 0, 0);
+                                        if (MODE == DKV) q[KT / 16] = make_uint4(0, 0, 0, 0);
+                                    }
+                                    for (int z = 0; z < 4; ++z) off &= off - 1;
+                                }
+                            }
+                            tc::fence_async_smem();
+                        }
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(bar + READY + s);
+                        if (c + 1 < n) fetch(p, c + 1);
+                        else if (p + 1 < passes) fetch(p + 1, 0);
+                    }
+                }
+                end_item(it);
+            }
+        } else if (warp == W_SG) {
+            // -------------------------------------------------------- S and G
+            const uint32_t id = tc::idesc_bf16(128, 64, false, false);
+            const uint64_t dR = tc::sdesc_sw128(tc::smem_u32(sm + OFF_R), 16, 1024);
+            const uint64_t dC = tc::sdesc_sw128(tc::smem_u32(sm + OFF_ST), 16, 1024);
+            int gu = 0;
+            bool ok = true;
+            for (int it = 0; ok && begin_item(it); ++it) {
+                const int rb = it & 1, nu = items[it % NIT].n * passes;
+                if (!ctl.wait_warp(RFULL + rb, (it >> 1) & 1)) break;
+                const uint64_t dA = tc::sdesc_add(dR, 2 * rb * TILE);
+                for (int u = 0; u < nu; ++u, ++gu) {
+                    const int s = gu % NST, x = gu % NSLOT;
+                    if (!ctl.wait_warp(READY + s, (gu / NST) & 1) ||
+                        (gu >= NSLOT && !ctl.wait_warp(SLOT + x, ((gu / NSLOT) - 1) & 1))) {
+                        ok = false;
+                        break;
+                    }
+                    tc::tc_fence_after();
+                    const uint64_t dB = tc::sdesc_add(dC, s * 2 * KT);
+                    if (tc::elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma_bf16(tm + 128 * x, tc::sdesc_add(dA, 32 * k), tc::sdesc_add(dB, 32 * k), id, k > 0);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma_bf16(tm + 128 * x + 64, tc::sdesc_add(dA, TILE + 32 * k),
+                                         tc::sdesc_add(dB, KT + 32 * k), id, k > 0);
+                        tc::tc_commit(bar + SGFULL + x);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (tc::elect_one()) tc::tc_commit(bar + REMPTY + rb);
+                end_item(it);
+            }
+            if (tc::elect_one()) tc::tc_commit(bar + DRAIN);
+            __syncwarp();
+            tc::mbar_wait(bar + DRAIN, 0, kWaitBudget);
+        } else {
+            // -------------------------------------------------------- the second products
+            const uint32_t id = tc::idesc_bf16(128, 64, false, true);
+            const uint64_t dC = tc::sdesc_sw128(tc::smem_u32(sm + OFF_ST), KT, 1024);
+            int gu = 0, na = 0;  // units, items with any
+            bool ok = true;
+            for (int it = 0; ok && begin_item(it); ++it) {
+                const int n = items[it % NIT].n, nu = n * passes;
+                const int skip = MODE == DQ && a.exact_d ? n : 0;  // units of the pass that only sums
+                const int ab = na % NACC;
+                for (int u = 0; u < nu; ++u, ++gu) {
+                    const int s = gu % NST, x = gu % NSLOT;
+                    if ((u == skip && na >= NACC && !ctl.wait_warp(ACCEMPTY + ab, ((na / NACC) - 1) & 1)) ||
+                        !ctl.wait_warp(DSFULL + x, (gu / NSLOT) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::tc_fence_after();
+                    const uint64_t dB = tc::sdesc_add(dC, s * 2 * KT);
+                    const uint32_t slot = tm + 128 * x, acc = tA + (MODE == DQ ? 64 * ab : 0);
+                    if (tc::elect_one()) {
+                        if (u >= skip) {
+                            // 16 columns of the chunk are 8 of TMEM; each half of a
+                            // slot's S (or G) keeps the columns it was formed from
+                            if (MODE == DQ) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    tc::mma_bf16_ts(acc, slot + 32 * (k >> 1) + 8 * (k & 1), tc::sdesc_add(dB, k * 2048), id,
+                                                    (u > skip || k > 0) ? 1u : 0u);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    tc::mma_bf16_ts(acc, slot + 32 * (k >> 1) + 8 * (k & 1),
+                                                    tc::sdesc_add(dB, KT + k * 2048), id, (u > 0 || k > 0) ? 1u : 0u);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    tc::mma_bf16_ts(acc + 64, slot + 64 + 32 * (k >> 1) + 8 * (k & 1),
+                                                    tc::sdesc_add(dB, k * 2048), id, (u > 0 || k > 0) ? 1u : 0u);
+                            }
+                        }
+                        tc::tc_commit(bar + SLOT + x);
+                        tc::tc_commit(bar + EMPTY + s);
+                        if (u == nu - 1) tc::tc_commit(bar + ACCFULL + ab);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (nu > 0) ++na;
+                end_item(it);
+            }
+            if (tc::elect_one()) tc::tc_commit(bar + DRAIN);
+            __syncwarp();
+            tc::mbar_wait(bar + DRAIN, 0, kWaitBudget);
+        }
+    } else {
+        // ------------------------------------------------------------ P and dS
+        reg_inc<REG_TEAM>();
+        const int qd = warp & 3, hf = (warp >> 2) & 1, team = warp >> 3;
+        const int r = qd * 32 + lane;
+        const uint32_t lanebase = (uint32_t)(qd * 32) << 16;
+        const uint64_t c2p = tc::pk2(a.c2, a.c2);
+        int gu = 0, na = 0, nx = 0;
+        bool ok = true;
+        for (int it = 0; ok && begin_item(it); ++it) {
+            const Item& w = items[it % NIT];
+            const int rb = it & 1, n = w.n, nu = n * passes;
+            if (!ctl.wait_warp(ROWFULL + rb, (it >> 1) & 1)) break;
+            Row row = rows[rb * 128 + r];
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar + ROWEMPTY + rb);
+            // columns that every row of the warp attends, and any
+            const int wlo = __reduce_max_sync(~0u, row.lo), whi = __reduce_min_sync(~0u, row.hi);
+            const int alo = __reduce_min_sync(~0u, row.hi < row.lo ? 0x7fffffff : row.lo);
+            const int ahi = __reduce_max_sync(~0u, row.hi < row.lo ? -1 : row.hi);
+            float sum = 0.f;  // of P G, with exact_d
+            const int skip = MODE == DQ && a.exact_d ? n : 0;
+            for (int u = 0; u < nu; ++u, ++gu) {
+                if (MODE == DQ && skip > 0 && u == skip) {  // the four shares of every row's D
+                    float* sh = xd + (nx & 1) * 512;
+                    sh[(2 * team + hf) * 128 + r] = sum;
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(bar + XDSUM);
+                    if (!ctl.wait_warp(XDSUM, nx & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    row.D = (sh[r] + sh[128 + r]) + (sh[256 + r] + sh[384 + r]);
+                }
+                if ((gu & 1) != team) continue;
+                const int s = gu % NST, x = gu % NSLOT, c = MODE == DQ && u >= skip ? u - skip : u % n;
+                if (!ctl.wait_warp(READY + s, (gu / NST) & 1) || !ctl.wait_warp(SGFULL + x, (gu / NSLOT) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc::tc_fence_after();
+                const uint32_t mS = tm + 128 * x + lanebase + 32 * hf, mG = mS + 64;
+                const int j0 = 64 * c + 32 * hf;
+                uint32_t on = words[2 * s + hf];
+                const bool full = j0 >= wlo && j0 + 31 <= whi && on == ~0u;
+                const bool any = j0 <= ahi && j0 + 31 >= alo;
+                const bool only_sum = MODE == DQ && u < skip;
+                if (!any) {
+                    if (!only_sum) {
+                        uint32_t z[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) z[j] = 0u;
+                        tc::tmem_st16(mS, z);
+                        if (MODE == DKV) tc::tmem_st16(mG, z);
+                        tc::tmem_wait_st();
+                    }
+                } else {
+                    if (!full) on &= range_bits(row.lo - j0, row.hi - j0);
+                    uint32_t pw[MODE == DKV ? 16 : 1], dw[16];
+                    const float* cv = cols + s * 128 + 32 * hf;
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {  // 16 columns at a time
+                        uint32_t sv[16], gv[16];
+                        tc::tmem_ld16(mS + 16 * z, sv);
+                        tc::tmem_ld16(mG + 16 * z, gv);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            uint64_t up, dp;
+                            if (MODE == DKV) {
+                                up = *reinterpret_cast<const uint64_t*>(cv + 16 * z + 2 * j);
+                                dp = *reinterpret_cast<const uint64_t*>(cv + 64 + 16 * z + 2 * j);
+                            } else {
+                                up = tc::pk2(row.u2, row.u2);
+                                dp = tc::pk2(row.D, row.D);
+                            }
+                            const uint64_t y =
+                                tc::fma2(tc::pk2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), c2p, up);
+                            const uint64_t d =
+                                tc::sub2(tc::pk2(__uint_as_float(gv[2 * j]), __uint_as_float(gv[2 * j + 1])), dp);
+                            float e0, e1, d0, d1;
+                            tc::upk2(y, e0, e1);
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                            tc::upk2(d, d0, d1);
+                            if (!full) {
+                                const bool k0 = (on >> (16 * z + 2 * j)) & 1u, k1 = (on >> (16 * z + 2 * j + 1)) & 1u;
+                                e0 = k0 ? e0 : 0.f;
+                                e1 = k1 ? e1 : 0.f;
+                                d0 = k0 ? d0 : 0.f;
+                                d1 = k1 ? d1 : 0.f;
+                            }
+                            d0 *= e0;
+                            d1 *= e1;
+                            if (MODE == DQ) sum += only_sum ? d0 + d1 : 0.f;
+                            dw[8 * z + j] = tc::pack_bf16(d0, d1);
+                            if (MODE == DKV) pw[MODE == DKV ? 8 * z + j : 0] = tc::pack_bf16(e0, e1);
+                        }
+                    }
+                    if (!only_sum) {
+                        if (MODE == DQ) {
+                            tc::tmem_st16(mS, dw);
+                        } else if constexpr (MODE == DKV) {
+                            tc::tmem_st16(mS, pw);
+                            tc::tmem_st16(mG, dw);
+                        }
+                        tc::tmem_wait_st();
+                    }
+                }
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bar + DSFULL + x);
+            }
+            if (!ok) break;
+            if (MODE == DQ && skip > 0) ++nx;
+            // the accumulators: this warp's lanes, 16 columns
+            const int ab = na % NACC, q4 = warp >> 2;
+            if (nu > 0) {
+                if (!ctl.wait_warp(ACCFULL + ab, (na / NACC) & 1)) break;
+                ++na;
+                tc::tc_fence_after();
+            }
+#pragma unroll
+            for (int k = 0; k < (MODE == DQ ? 1 : 2); ++k) {
+                uint32_t o[16];
+                if (nu > 0) {
+                    tc::tmem_ld16(tA + (MODE == DQ ? 64 * ab : 64 * k) + lanebase + 16 * q4, o);
+                    tc::tmem_wait_ld();
+                }
+                const float f = MODE == DKV && k == 0 ? 1.f : a.c;
+                __nv_bfloat16* out = nullptr;
+                if (MODE == DQ) {
+                    const int g = r / a.nq, t = w.r0 + r % a.nq;
+                    if (g < a.G && t < a.Lq) out = a.dq.at<__nv_bfloat16>(w.b, w.hk * a.G + g, t);
+                } else if (w.r0 + r < a.Lk) {
+                    out = (k == 0 ? a.dv : a.dk).at<__nv_bfloat16>(w.b, w.hk, w.r0 + r);
+                }
+                if (out) {
+                    uint4* p = reinterpret_cast<uint4*>(out + 16 * q4);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            y[e] = nu > 0 ? tc::pack_bf16(__uint_as_float(o[8 * j + 2 * e]) * f,
+                                                          __uint_as_float(o[8 * j + 2 * e + 1]) * f)
+                                          : 0u;
+                        p[j] = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+                __syncwarp();
+            }
+            if (nu > 0) {
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bar + ACCEMPTY + ab);
+            }
+            if (MODE == DQ && a.exact_d && q4 == 0) {
+                const int g = r / a.nq, t = w.r0 + r % a.nq;
+                if (g < a.G && t < a.Lq) a.D[((long long)w.b * a.Hq + w.hk * a.G + g) * a.Lq + t] = row.D;
+            }
+            end_item(it);
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc::tc_fence_after();
+        tc::tmem_dealloc(tm, 512);
+    }
+}
+
+}  // namespace bwd
+}  // namespace tcf
+}  // namespace sm
+}  // namespace sa
