@@ -14,9 +14,10 @@
 // from, from where the second products read them as their A operand.  Two teams
 // take the units in turn.  One warp issues S and G, another the second products
 // (one thread for all that add into an accumulator); a loader brings the tiles,
-// and an aux warp prepares each item's rows (D = dO . O among them) and each
-// chunk's columns (mask words; u and D of queries; zeroed operand rows of tokens
-// that are not in use, as 0 times what they hold need not be 0).
+// and an aux warp prepares each chunk's columns (mask words; u and D of queries;
+// zeroed operand rows of tokens that are not in use, as 0 times what they hold
+// need not be 0).  D = dO . O is formed by the teams' warps at an item's start, a
+// quarter of the channels each; one aux warp for all rows took 20 us an item.
 #pragma once
 
 #include "softmax_tc.cuh"
@@ -39,26 +40,20 @@ struct Item {
     // columns vlo .. vhi (absolute) are in some row's band; n chunks per head
     long long first;
 };
-struct Row {
-    float u2, D;
-    int lo, hi;  // columns in the band, relative to c0
-};
 
 constexpr int OFF_R = 0;                        // two buffers of two row tiles
 constexpr int OFF_ST = OFF_R + 4 * TILE;        // stages of two chunk tiles
 constexpr int OFF_ITEM = OFF_ST + NST * 2 * KT;
-constexpr int OFF_ROW = OFF_ITEM + NIT * (int)sizeof(Item);
-constexpr int OFF_COL = OFF_ROW + 2 * 128 * (int)sizeof(Row);  // per stage: u2[64], D[64]
+constexpr int OFF_COL = OFF_ITEM + NIT * (int)sizeof(Item);  // per stage: u2[64], D[64]
 constexpr int OFF_XD = OFF_COL + NST * 512;     // two buffers of shares of D, [4][128]
 constexpr int OFF_WORDS = OFF_XD + 4096;
 constexpr int OFF_BAR = OFF_WORDS + NST * 8;
-enum { RFULL = 0, REMPTY = 2, IFULL = 4, IEMPTY = IFULL + NIT, ROWFULL = IEMPTY + NIT, ROWEMPTY = ROWFULL + 2,
-       SGFULL = ROWEMPTY + 2, DSFULL = SGFULL + NSLOT, SLOT = DSFULL + NSLOT, ACCFULL = SLOT + NSLOT,
+enum { RFULL = 0, REMPTY = 2, IFULL = 4, IEMPTY = IFULL + NIT, SGFULL = IEMPTY + NIT, DSFULL = SGFULL + NSLOT, SLOT = DSFULL + NSLOT, ACCFULL = SLOT + NSLOT,
        ACCEMPTY = ACCFULL + 2, XDSUM = ACCEMPTY + 2, DRAIN = XDSUM + 1, FULL = DRAIN + 1, READY = FULL + NST,
        EMPTY = READY + NST, NBAR = EMPTY + NST };
 constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
 static_assert(SMEM <= 227 * 1024, "shared memory");
-static_assert(sizeof(Item) % 8 == 0 && OFF_ROW % 16 == 0 && OFF_COL % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
+static_assert(sizeof(Item) % 8 == 0 && OFF_COL % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
 
 struct Maps {
     CUtensorMap R1, R2, C1, C2;  // DQ: Q, dO, K, V;  DKV: K, V, Q, dO
@@ -102,7 +97,6 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tbase + 1);
     uint32_t* words = reinterpret_cast<uint32_t*>(sm + OFF_WORDS);
     Item* items = reinterpret_cast<Item*>(sm + OFF_ITEM);
-    Row* rows = reinterpret_cast<Row*>(sm + OFF_ROW);
     float* cols = reinterpret_cast<float*>(sm + OFF_COL);
     float* xd = reinterpret_cast<float*>(sm + OFF_XD);
     Ctl ctl{bar, abort_flag, a.status};
@@ -112,9 +106,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar + RFULL + i, 1);
-            tc::mbar_init(bar + REMPTY + i, 2);
-            tc::mbar_init(bar + ROWFULL + i, 1);
-            tc::mbar_init(bar + ROWEMPTY + i, 16);
+            tc::mbar_init(bar + REMPTY + i, MODE == DQ ? 17 : 1);  // the MMAs, and the warps that read dO
             tc::mbar_init(bar + ACCFULL + i, 1);
             tc::mbar_init(bar + ACCEMPTY + i, 16);
         }
@@ -208,86 +200,13 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             }
             __syncwarp();
         } else if (warp == W_AUX) {
-            // -------------------------------------------------------- rows and columns
+            // -------------------------------------------------------- columns
             int gu = 0;
             bool ok = true;
             for (int it = 0; ok && begin_item(it); ++it) {
                 const Item& w = items[it % NIT];
-                const int rb = it & 1, b = w.b, hk = w.hk, n = w.n, c0 = w.c0;
+                const int b = w.b, hk = w.hk, n = w.n, c0 = w.c0;
                 const long long first = w.first;
-                if (it >= 2 && !ctl.wait_warp(ROWEMPTY + rb, ((it >> 1) - 1) & 1)) break;
-                if (!ctl.wait_warp(RFULL + rb, (it >> 1) & 1)) break;
-                Row* row = rows + rb * 128;
-                if (MODE == DQ) {
-                    const uint8_t* g = sm + OFF_R + (2 * rb + 1) * TILE;
-#pragma unroll 1
-                    for (int r0 = 0; r0 < 128; r0 += 16) {  // four rows at a time, eight lanes each
-                        uint4 o[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int r = r0 + 4 * e + (lane >> 3), t = w.r0 + r % a.nq;
-                            o[e] = make_uint4(0, 0, 0, 0);
-                            if (!a.exact_d && r / a.nq < a.G && t < a.Lq)
-                                o[e] = *reinterpret_cast<const uint4*>(
-                                    a.o.at<__nv_bfloat16>(b, hk * a.G + r / a.nq, t) + 8 * (lane & 7));
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int r = r0 + 4 * e + (lane >> 3), t = w.r0 + r % a.nq, gh = r / a.nq;
-                            const uint4 y = *reinterpret_cast<const uint4*>(g + tc::sw128_off(r, lane & 7));
-                            const __nv_bfloat162* po = reinterpret_cast<const __nv_bfloat162*>(&o[e]);
-                            const __nv_bfloat162* py = reinterpret_cast<const __nv_bfloat162*>(&y);
-                            float dot = 0.f;
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) {
-                                const float2 f = __bfloat1622float2(po[z]), k = __bfloat1622float2(py[z]);
-                                dot = fmaf(f.x, k.x, fmaf(f.y, k.y, dot));
-                            }
-#pragma unroll
-                            for (int z = 4; z; z >>= 1) dot += __shfl_xor_sync(~0u, dot, z);
-                            if ((lane & 7) == 0) {
-                                Row x;
-                                x.u2 = x.D = 0.f;
-                                x.lo = 0;
-                                x.hi = -1;
-                                if (gh < a.G && t < a.Lq) {
-                                    const long long at = ((long long)b * a.Hq + hk * a.G + gh) * a.Lq + t;
-                                    const long long p = first + t;
-                                    if (p >= 0 && p < a.Lk && a.live(b, (int)p)) {
-                                        a.keys(p, x.lo, x.hi);
-                                        x.lo -= c0;
-                                        x.hi -= c0;
-                                        x.u2 = a.u[at] * kLog2e;
-                                        x.D = dot;
-                                    }
-                                    if (!a.exact_d) a.D[at] = x.D;
-                                }
-                                row[r] = x;
-                            }
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = 32 * e + lane, j = w.r0 + r;
-                        Row x;
-                        x.u2 = x.D = 0.f;
-                        x.lo = 0;
-                        x.hi = -1;
-                        if (j < a.Lk && a.live(b, j)) {
-                            // queries j - R .. j + W, as columns; the words end them at the last query
-                            const long long lo = (long long)j - a.R - first - c0, hi = (long long)j + a.W - first - c0;
-                            x.lo = (int)(lo < 0 ? 0 : lo > (1 << 30) ? (1 << 30) : lo);
-                            x.hi = (int)(hi < -1 ? -1 : hi > (1 << 30) ? (1 << 30) : hi);
-                        }
-                        row[r] = x;
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) {
-                    tc::mbar_arrive(bar + ROWFULL + rb);
-                    tc::mbar_arrive(bar + REMPTY + rb);
-                }
                 // the columns of a chunk: this lane's two
                 uint32_t bits[2];
                 float cu[2], cD[2];
@@ -449,36 +368,88 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
     } else {
         // ------------------------------------------------------------ P and dS
         reg_inc<REG_TEAM>();
-        const int qd = warp & 3, hf = (warp >> 2) & 1, team = warp >> 3;
+        const int qd = warp & 3, hf = (warp >> 2) & 1, team = warp >> 3, q4 = warp >> 2;
         const int r = qd * 32 + lane;
+        const int g = MODE == DQ ? r / a.nq : 0, iq = MODE == DQ ? r % a.nq : r;
         const uint32_t lanebase = (uint32_t)(qd * 32) << 16;
         const uint64_t c2p = tc::pk2(a.c2, a.c2);
         int gu = 0, na = 0, nx = 0;
         bool ok = true;
+        // The sum over the four warps that hold a row's columns.  Two buffers: to
+        // reach the one after the next, every warp has read this one.
+        auto share_d = [&](float x, float& total) -> bool {
+            float* sh = xd + (nx & 1) * 512;
+            sh[q4 * 128 + r] = x;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(bar + XDSUM);
+            if (!ctl.wait_warp(XDSUM, nx & 1)) return false;
+            ++nx;
+            total = (sh[r] + sh[128 + r]) + (sh[256 + r] + sh[384 + r]);
+            return true;
+        };
         for (int it = 0; ok && begin_item(it); ++it) {
             const Item& w = items[it % NIT];
             const int rb = it & 1, n = w.n, nu = n * passes;
-            if (!ctl.wait_warp(ROWFULL + rb, (it >> 1) & 1)) break;
-            Row row = rows[rb * 128 + r];
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(bar + ROWEMPTY + rb);
+            // this row: its columns in the band, relative to chunk 0
+            float u2 = 0.f, D = 0.f;
+            int lo = 0, hi = -1;
+            const int i = w.r0 + iq;  // query or key
+            const bool exists = MODE == DQ ? g < a.G && i < a.Lq : i < a.Lk;
+            const long long at = MODE == DQ ? ((long long)w.b * a.Hq + w.hk * a.G + g) * a.Lq + i : 0;
+            if (MODE == DQ) {
+                const bool dot = !a.exact_d;
+                uint4 o[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                bool in = false;
+                if (exists) {
+                    const long long p = w.first + i;
+                    if (p >= 0 && p < a.Lk && a.live(w.b, (int)p)) {
+                        in = true;
+                        a.keys(p, lo, hi);
+                        lo -= w.c0;
+                        hi -= w.c0;
+                        u2 = a.u[at] * kLog2e;
+                        if (dot) {
+                            const uint4* po = reinterpret_cast<const uint4*>(
+                                a.o.at<__nv_bfloat16>(w.b, w.hk * a.G + g, i) + 16 * q4);
+                            o[0] = po[0];
+                            o[1] = po[1];
+                        }
+                    }
+                }
+                if (!ctl.wait_warp(RFULL + rb, (it >> 1) & 1)) break;
+                if (dot) {  // D = dO . O, a quarter of the channels here
+                    const uint8_t* dO = sm + OFF_R + (2 * rb + 1) * TILE;
+                    float x = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint4 y = *reinterpret_cast<const uint4*>(dO + tc::sw128_off(r, 2 * q4 + e));
+                        const __nv_bfloat162* po = reinterpret_cast<const __nv_bfloat162*>(&o[e]);
+                        const __nv_bfloat162* py = reinterpret_cast<const __nv_bfloat162*>(&y);
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const float2 f = __bfloat1622float2(po[z]), k = __bfloat1622float2(py[z]);
+                            x = fmaf(f.x, k.x, fmaf(f.y, k.y, x));
+                        }
+                    }
+                    if (!share_d(in ? x : 0.f, D)) break;
+                }
+                if (lane == 0) tc::mbar_arrive(bar + REMPTY + rb);
+            } else if (exists && a.live(w.b, i)) {
+                // queries i - R .. i + W; the words end them at the last one
+                const long long l = (long long)i - a.R - w.first - w.c0, h = (long long)i + a.W - w.first - w.c0;
+                lo = (int)(l < 0 ? 0 : l > (1 << 30) ? (1 << 30) : l);
+                hi = (int)(h < -1 ? -1 : h > (1 << 30) ? (1 << 30) : h);
+            }
             // columns that every row of the warp attends, and any
-            const int wlo = __reduce_max_sync(~0u, row.lo), whi = __reduce_min_sync(~0u, row.hi);
-            const int alo = __reduce_min_sync(~0u, row.hi < row.lo ? 0x7fffffff : row.lo);
-            const int ahi = __reduce_max_sync(~0u, row.hi < row.lo ? -1 : row.hi);
+            const int wlo = __reduce_max_sync(~0u, lo), whi = __reduce_min_sync(~0u, hi);
+            const int alo = __reduce_min_sync(~0u, hi < lo ? 0x7fffffff : lo);
+            const int ahi = __reduce_max_sync(~0u, hi < lo ? -1 : hi);
             float sum = 0.f;  // of P G, with exact_d
             const int skip = MODE == DQ && a.exact_d ? n : 0;
             for (int u = 0; u < nu; ++u, ++gu) {
-                if (MODE == DQ && skip > 0 && u == skip) {  // the four shares of every row's D
-                    float* sh = xd + (nx & 1) * 512;
-                    sh[(2 * team + hf) * 128 + r] = sum;
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(bar + XDSUM);
-                    if (!ctl.wait_warp(XDSUM, nx & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    row.D = (sh[r] + sh[128 + r]) + (sh[256 + r] + sh[384 + r]);
+                if (MODE == DQ && skip > 0 && u == skip && !share_d(sum, D)) {
+                    ok = false;
+                    break;
                 }
                 if ((gu & 1) != team) continue;
                 const int s = gu % NST, x = gu % NSLOT, c = MODE == DQ && u >= skip ? u - skip : u % n;
@@ -503,7 +474,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                         tc::tmem_wait_st();
                     }
                 } else {
-                    if (!full) on &= range_bits(row.lo - j0, row.hi - j0);
+                    if (!full) on &= range_bits(lo - j0, hi - j0);
                     uint32_t pw[MODE == DKV ? 16 : 1], dw[16];
                     const float* cv = cols + s * 128 + 32 * hf;
 #pragma unroll
@@ -519,8 +490,8 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                                 up = *reinterpret_cast<const uint64_t*>(cv + 16 * z + 2 * j);
                                 dp = *reinterpret_cast<const uint64_t*>(cv + 64 + 16 * z + 2 * j);
                             } else {
-                                up = tc::pk2(row.u2, row.u2);
-                                dp = tc::pk2(row.D, row.D);
+                                up = tc::pk2(u2, u2);
+                                dp = tc::pk2(D, D);
                             }
                             const uint64_t y =
                                 tc::fma2(tc::pk2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), c2p, up);
@@ -560,9 +531,8 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                 if (lane == 0) tc::mbar_arrive(bar + DSFULL + x);
             }
             if (!ok) break;
-            if (MODE == DQ && skip > 0) ++nx;
             // the accumulators: this warp's lanes, 16 columns
-            const int ab = na % NACC, q4 = warp >> 2;
+            const int ab = na % NACC;
             if (nu > 0) {
                 if (!ctl.wait_warp(ACCFULL + ab, (na / NACC) & 1)) break;
                 ++na;
@@ -577,12 +547,9 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                 }
                 const float f = MODE == DKV && k == 0 ? 1.f : a.c;
                 __nv_bfloat16* out = nullptr;
-                if (MODE == DQ) {
-                    const int g = r / a.nq, t = w.r0 + r % a.nq;
-                    if (g < a.G && t < a.Lq) out = a.dq.at<__nv_bfloat16>(w.b, w.hk * a.G + g, t);
-                } else if (w.r0 + r < a.Lk) {
-                    out = (k == 0 ? a.dv : a.dk).at<__nv_bfloat16>(w.b, w.hk, w.r0 + r);
-                }
+                if (exists)
+                    out = MODE == DQ ? a.dq.at<__nv_bfloat16>(w.b, w.hk * a.G + g, i)
+                                     : (k == 0 ? a.dv : a.dk).at<__nv_bfloat16>(w.b, w.hk, i);
                 if (out) {
                     uint4* p = reinterpret_cast<uint4*>(out + 16 * q4);
 #pragma unroll
@@ -603,10 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bar + ACCEMPTY + ab);
             }
-            if (MODE == DQ && a.exact_d && q4 == 0) {
-                const int g = r / a.nq, t = w.r0 + r % a.nq;
-                if (g < a.G && t < a.Lq) a.D[((long long)w.b * a.Hq + w.hk * a.G + g) * a.Lq + t] = row.D;
-            }
+            if (MODE == DQ && exists && q4 == 0) a.D[at] = D;
             end_item(it);
         }
     }
