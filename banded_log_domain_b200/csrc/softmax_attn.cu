@@ -179,7 +179,7 @@ cudaError_t bwd_simt(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cu
     return launch(sm::simt::k_bwd_kv<float>, BH * pl.nktile, sm::simt::THREADS, sm::simt::smem_bytes(6), st, a);
 }
 
-template <int MODE>
+template <int MODE, bool EXACT>
 cudaError_t bwd_tc(const sa_softmax_params* p, const sm::Args& a, long long items, cudaStream_t st) {
     using namespace sm::tcf::bwd;
     Maps maps;
@@ -192,8 +192,8 @@ cudaError_t bwd_tc(const sa_softmax_params* p, const sm::Args& a, long long item
              make_map(&maps.C1, a.q, p->B, p->Hq, p->Lq, 64, 1) && make_map(&maps.C2, a.dO, p->B, p->Hq, p->Lq, 64, 1);
     if (!ok) return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)std::min<long long>(items, sm_count());
-    cudaError_t e = cudaFuncSetAttribute(tc_bwd<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    if (e == cudaSuccess) e = launch_pdl(tc_bwd<MODE>, dim3(grid), dim3(THREADS), SMEM, st, a, maps, (int)items);
+    cudaError_t e = cudaFuncSetAttribute(tc_bwd<MODE, EXACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e == cudaSuccess) e = launch_pdl(tc_bwd<MODE, EXACT>, dim3(grid), dim3(THREADS), SMEM, st, a, maps, (int)items);
     return e;
 }
 
@@ -209,8 +209,9 @@ cudaError_t bwd_launch(const sa_softmax_params* p, const Plan& pl, sm::Args& a, 
     const long long BH = (long long)p->B * p->Hk;
     a.nq = pl.nq;
     a.ntile = (p->Lq + a.nq - 1) / a.nq;
-    const cudaError_t e = bwd_tc<sm::tcf::bwd::DQ>(p, a, BH * a.ntile, st);
-    return e != cudaSuccess ? e : bwd_tc<sm::tcf::bwd::DKV>(p, a, BH * ((p->Lk + 127) / 128), st);
+    const cudaError_t e = a.exact_d ? bwd_tc<sm::tcf::bwd::DQ, true>(p, a, BH * a.ntile, st)
+                                    : bwd_tc<sm::tcf::bwd::DQ, false>(p, a, BH * a.ntile, st);
+    return e != cudaSuccess ? e : bwd_tc<sm::tcf::bwd::DKV, false>(p, a, BH * ((p->Lk + 127) / 128), st);
 }
 
 }  // namespace

@@ -88,7 +88,8 @@ __device__ __forceinline__ void make_item(const Args& a, int idx, Item& w) {
     w.n = (hi - lo + 64) / 64;  // 0 when empty
 }
 
-template <int MODE>
+// EXACT (DQ): D is summed in a first pass over the chunks.
+template <int MODE, bool EXACT>
 __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_constant__ Maps maps, int nitems) {
     extern __shared__ uint8_t smraw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smraw + 1023) & ~(uintptr_t)1023);
@@ -149,9 +150,9 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar + IEMPTY + it % NIT);
     };
-    // units of an item: its chunks, for each head of the group (DKV), or twice (DQ
-    // with exact_d: first D = sum_j P G, then the gradient)
-    const int passes = MODE == DKV ? a.G : a.exact_d ? 2 : 1;
+    // units of an item: its chunks, for each head of the group (DKV), or twice
+    // (EXACT: first D = sum_j P G, then the gradient)
+    const int passes = MODE == DKV ? a.G : EXACT ? 2 : 1;
 
     if (warp >= 16) {
         reg_dec<REG_OTHER>();
@@ -205,26 +206,22 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             bool ok = true;
             for (int it = 0; ok && begin_item(it); ++it) {
                 const Item& w = items[it % NIT];
-                const int b = w.b, hk = w.hk, n = w.n, c0 = w.c0;
-                const long long first = w.first;
+                const int n = w.n, last = w.vhi - w.c0;  // columns 0 .. last, from c0 on
+                // mask of column 0, u and D of the group's first head at column 0
+                const uint8_t* pm = a.mask ? a.mask + (long long)w.b * a.Lk + w.c0 + (MODE == DKV ? w.first : 0) : nullptr;
+                const long long at = MODE == DKV ? ((long long)w.b * a.Hq + w.hk * a.G) * a.Lq + w.c0 : 0;
                 // the columns of a chunk: this lane's two
                 uint32_t bits[2];
                 float cu[2], cD[2];
                 auto fetch = [&](int p, int c) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int j = c0 + 64 * c + 32 * k + lane;
-                        bool on = j >= w.vlo && j <= w.vhi;
-                        cu[k] = cD[k] = 0.f;
-                        if (MODE == DQ) {
-                            on = on && a.live(b, j);
-                        } else {
-                            on = on && a.live(b, (int)(first + j));
-                            if (on) {
-                                const long long at = ((long long)b * a.Hq + hk * a.G + p) * a.Lq + j;
-                                cu[k] = a.u[at] * kLog2e;
-                                cD[k] = a.D[at];
-                            }
+                        const int j = 64 * c + 32 * k + lane;
+                        const bool on = j <= last && (pm == nullptr || pm[j] != 0);
+                        if (MODE == DKV) {
+                            const long long x = at + (long long)p * a.Lq + j;
+                            cu[k] = on ? a.u[x] * kLog2e : 0.f;
+                            cD[k] = on ? a.D[x] : 0.f;
                         }
                         bits[k] = __ballot_sync(~0u, on);
                     }
@@ -319,7 +316,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             bool ok = true;
             for (int it = 0; ok && begin_item(it); ++it) {
                 const int n = items[it % NIT].n, nu = n * passes;
-                const int skip = MODE == DQ && a.exact_d ? n : 0;  // units of the pass that only sums
+                const int skip = EXACT ? n : 0;  // units of the pass that only sums
                 const int ab = na % NACC;
                 for (int u = 0; u < nu; ++u, ++gu) {
                     const int s = gu % NST, x = gu % NSLOT;
@@ -397,7 +394,6 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             const bool exists = MODE == DQ ? g < a.G && i < a.Lq : i < a.Lk;
             const long long at = MODE == DQ ? ((long long)w.b * a.Hq + w.hk * a.G + g) * a.Lq + i : 0;
             if (MODE == DQ) {
-                const bool dot = !a.exact_d;
                 uint4 o[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
                 bool in = false;
                 if (exists) {
@@ -408,7 +404,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                         lo -= w.c0;
                         hi -= w.c0;
                         u2 = a.u[at] * kLog2e;
-                        if (dot) {
+                        if (!EXACT) {
                             const uint4* po = reinterpret_cast<const uint4*>(
                                 a.o.at<__nv_bfloat16>(w.b, w.hk * a.G + g, i) + 16 * q4);
                             o[0] = po[0];
@@ -417,7 +413,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                     }
                 }
                 if (!ctl.wait_warp(RFULL + rb, (it >> 1) & 1)) break;
-                if (dot) {  // D = dO . O, a quarter of the channels here
+                if (!EXACT) {  // D = dO . O, a quarter of the channels here
                     const uint8_t* dO = sm + OFF_R + (2 * rb + 1) * TILE;
                     float x = 0.f;
 #pragma unroll
@@ -435,47 +431,52 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                 }
                 if (lane == 0) tc::mbar_arrive(bar + REMPTY + rb);
             } else if (exists && a.live(w.b, i)) {
-                // queries i - R .. i + W; the words end them at the last one
+                // queries i - R .. i + W of the item's vlo .. vhi
                 const long long l = (long long)i - a.R - w.first - w.c0, h = (long long)i + a.W - w.first - w.c0;
-                lo = (int)(l < 0 ? 0 : l > (1 << 30) ? (1 << 30) : l);
-                hi = (int)(h < -1 ? -1 : h > (1 << 30) ? (1 << 30) : h);
+                const int last = w.vhi - w.c0;
+                lo = (int)(l < 0 ? 0 : l > last ? last + 1 : l);
+                hi = (int)(h < -1 ? -1 : h > last ? last : h);
             }
             // columns that every row of the warp attends, and any
             const int wlo = __reduce_max_sync(~0u, lo), whi = __reduce_min_sync(~0u, hi);
             const int alo = __reduce_min_sync(~0u, hi < lo ? 0x7fffffff : lo);
             const int ahi = __reduce_max_sync(~0u, hi < lo ? -1 : hi);
-            float sum = 0.f;  // of P G, with exact_d
-            const int skip = MODE == DQ && a.exact_d ? n : 0;
-            for (int u = 0; u < nu; ++u, ++gu) {
-                if (MODE == DQ && skip > 0 && u == skip && !share_d(sum, D)) {
-                    ok = false;
-                    break;
+            // This team's units: every second one of the block's.  c: the unit's chunk.
+            float sum = 0.f;  // EXACT: of P G
+            bool summed = !EXACT || n == 0;
+            int c = (gu ^ team) & 1;
+            for (int u = c;; u += 2, c += 2) {
+                if (EXACT && !summed && u >= n) {  // the first pass is over
+                    if (!share_d(sum, D)) {
+                        ok = false;
+                        break;
+                    }
+                    summed = true;
                 }
-                if ((gu & 1) != team) continue;
-                const int s = gu % NST, x = gu % NSLOT, c = MODE == DQ && u >= skip ? u - skip : u % n;
-                if (!ctl.wait_warp(READY + s, (gu / NST) & 1) || !ctl.wait_warp(SGFULL + x, (gu / NSLOT) & 1)) {
+                if (u >= nu) break;
+                while (c >= n) c -= n;
+                const int gv0 = gu + u, s = gv0 % NST, x = gv0 % NSLOT;
+                if (((MODE == DKV || a.mask) && !ctl.wait_warp(READY + s, (gv0 / NST) & 1)) ||
+                    !ctl.wait_warp(SGFULL + x, (gv0 / NSLOT) & 1)) {
                     ok = false;
                     break;
                 }
                 tc::tc_fence_after();
                 const uint32_t mS = tm + 128 * x + lanebase + 32 * hf, mG = mS + 64;
                 const int j0 = 64 * c + 32 * hf;
-                uint32_t on = words[2 * s + hf];
+                uint32_t on = a.mask ? words[2 * s + hf] : ~0u;
                 const bool full = j0 >= wlo && j0 + 31 <= whi && on == ~0u;
                 const bool any = j0 <= ahi && j0 + 31 >= alo;
-                const bool only_sum = MODE == DQ && u < skip;
+                const bool only_sum = EXACT && !summed;
+                uint32_t pw[MODE == DKV ? 16 : 1], dw[16];
                 if (!any) {
-                    if (!only_sum) {
-                        uint32_t z[16];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) z[j] = 0u;
-                        tc::tmem_st16(mS, z);
-                        if (MODE == DKV) tc::tmem_st16(mG, z);
-                        tc::tmem_wait_st();
+                    for (int j = 0; j < 16; ++j) dw[j] = 0u;
+                    if constexpr (MODE == DKV) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) pw[j] = 0u;
                     }
                 } else {
-                    if (!full) on &= range_bits(lo - j0, hi - j0);
-                    uint32_t pw[MODE == DKV ? 16 : 1], dw[16];
                     const float* cv = cols + s * 128 + 32 * hf;
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {  // 16 columns at a time
@@ -483,54 +484,60 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                         tc::tmem_ld16(mS + 16 * z, sv);
                         tc::tmem_ld16(mG + 16 * z, gv);
                         tc::tmem_wait_ld();
+                        if (!full) {
+                            // scores of -inf give P = 0; G must be finite for dS = 0
+                            const uint32_t m = on & range_bits(lo - j0, hi - j0);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            uint64_t up, dp;
+                            for (int j = 0; j < 16; ++j)
+                                if (!((m >> (16 * z + j)) & 1u)) {
+                                    sv[j] = 0xff800000u;
+                                    gv[j] = 0u;
+                                }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; j += 2) {
+                            ulonglong2 up, dp;
                             if (MODE == DKV) {
-                                up = *reinterpret_cast<const uint64_t*>(cv + 16 * z + 2 * j);
-                                dp = *reinterpret_cast<const uint64_t*>(cv + 64 + 16 * z + 2 * j);
+                                up = *reinterpret_cast<const ulonglong2*>(cv + 16 * z + 2 * j);
+                                dp = *reinterpret_cast<const ulonglong2*>(cv + 64 + 16 * z + 2 * j);
                             } else {
-                                up = tc::pk2(u2, u2);
-                                dp = tc::pk2(D, D);
+                                up.x = up.y = tc::pk2(u2, u2);
+                                dp.x = dp.y = tc::pk2(D, D);
                             }
-                            const uint64_t y =
-                                tc::fma2(tc::pk2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), c2p, up);
-                            const uint64_t d =
-                                tc::sub2(tc::pk2(__uint_as_float(gv[2 * j]), __uint_as_float(gv[2 * j + 1])), dp);
-                            float e0, e1, d0, d1;
-                            tc::upk2(y, e0, e1);
-                            e0 = ex2(e0);
-                            e1 = ex2(e1);
-                            tc::upk2(d, d0, d1);
-                            if (!full) {
-                                const bool k0 = (on >> (16 * z + 2 * j)) & 1u, k1 = (on >> (16 * z + 2 * j + 1)) & 1u;
-                                e0 = k0 ? e0 : 0.f;
-                                e1 = k1 ? e1 : 0.f;
-                                d0 = k0 ? d0 : 0.f;
-                                d1 = k1 ? d1 : 0.f;
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const int k = 2 * (j + y);
+                                const uint64_t xx = tc::fma2(
+                                    tc::pk2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), c2p, y ? up.y : up.x);
+                                const uint64_t d = tc::sub2(tc::pk2(__uint_as_float(gv[k]), __uint_as_float(gv[k + 1])),
+                                                            y ? dp.y : dp.x);
+                                float e0, e1, d0, d1;
+                                tc::upk2(xx, e0, e1);
+                                e0 = ex2(e0);
+                                e1 = ex2(e1);
+                                tc::upk2(mul2(d, tc::pk2(e0, e1)), d0, d1);
+                                if (EXACT && only_sum) sum += d0 + d1;
+                                dw[8 * z + j + y] = tc::pack_bf16(d0, d1);
+                                if constexpr (MODE == DKV) pw[8 * z + j + y] = tc::pack_bf16(e0, e1);
                             }
-                            d0 *= e0;
-                            d1 *= e1;
-                            if (MODE == DQ) sum += only_sum ? d0 + d1 : 0.f;
-                            dw[8 * z + j] = tc::pack_bf16(d0, d1);
-                            if (MODE == DKV) pw[MODE == DKV ? 8 * z + j : 0] = tc::pack_bf16(e0, e1);
                         }
                     }
-                    if (!only_sum) {
-                        if (MODE == DQ) {
-                            tc::tmem_st16(mS, dw);
-                        } else if constexpr (MODE == DKV) {
-                            tc::tmem_st16(mS, pw);
-                            tc::tmem_st16(mG, dw);
-                        }
-                        tc::tmem_wait_st();
+                }
+                if (!only_sum) {
+                    if constexpr (MODE == DKV) {
+                        tc::tmem_st16(mS, pw);
+                        tc::tmem_st16(mG, dw);
+                    } else {
+                        tc::tmem_st16(mS, dw);
                     }
+                    tc::tmem_wait_st();
                 }
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bar + DSFULL + x);
             }
             if (!ok) break;
+            gu += nu;
             // the accumulators: this warp's lanes, 16 columns
             const int ab = na % NACC;
             if (nu > 0) {
