@@ -222,6 +222,11 @@ def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _raw_stream(device):
+    """The current stream's handle, without the stream object that :func:`_stream` makes."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _on(device, fn, *args):
     """Calls the C entry point ``fn`` with ``device`` current (the library
     validates every pointer against the current device and launches there)."""
@@ -660,48 +665,61 @@ def bias_certificate(q, k, v, dO, *, N, Rs=(0, 1, 2, 4), tau=1e-5, W, eps, mask=
 _DTYPES = {torch.float32: SA_F32, torch.bfloat16: SA_BF16}
 
 
-def _strided(p, **tensors):
-    """Writes the tensors' batch, head and token strides into the params ``p``
-    (the library rejects those that are not multiples of 16 bytes)."""
-    for name, t in tensors.items():
-        st, n = t.stride(), t.shape
-        if st[3] != 1 and n[3] > 1:
-            raise ValueError(f"{name}: the last dimension must be contiguous")
-        if (st[0] <= 0 and n[0] > 1) or (st[1] <= 0 and n[1] > 1) or (st[2] <= 0 and n[2] > 1):
-            raise ValueError(f"{name}: expanded dimensions are not supported")
-        setattr(p, name + "_stride", _S3(*st[:3]))
+def _strided(p, name, t):
+    """Writes the batch, head and token strides of ``t`` into the params ``p`` (zeros,
+    as they are, mean contiguous; the library rejects strides that are not
+    multiples of 16 bytes)."""
+    if t.is_contiguous():
+        return
+    st, n = t.stride(), t.shape
+    if st[3] != 1 and n[3] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if (st[0] <= 0 and n[0] > 1) or (st[1] <= 0 and n[1] > 1) or (st[2] <= 0 and n[2] > 1):
+        raise ValueError(f"{name}: expanded dimensions are not supported")
+    setattr(p, name + "_stride", _S3(*st[:3]))
 
 
-def _same(what, like, shape, **tensors):
-    """Every tensor of ``shape`` with ``like``'s dtype and device."""
-    for name, t in tensors.items():
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}, {what}")
-        if t.dtype != like.dtype or t.device != like.device:
-            raise ValueError(f"{name}: {t.dtype} on {t.device}, not {like.dtype} on {like.device}")
+def _same(name, t, like, shape):
+    """``t`` has ``shape`` and the dtype and device of ``like``."""
+    if t.shape != shape or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, not {like.dtype} "
+                         f"{tuple(shape)} on {like.device}")
 
 
 def _aux(name, t, dtype, shape, device):
-    """An optional contiguous tensor of a fixed dtype and shape."""
+    """A contiguous tensor of a fixed dtype and shape; its address, or None for None."""
     if t is None:
-        return
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{name}: {dtype} {tuple(shape)} on {device} expected")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
 
 
-def _softmax_params(q, k, v, W, eps, causal, mask, q_pos):
+def _made(name, t, like, p):
+    """An output like ``like``: ``t``, checked, or a new contiguous tensor."""
+    if t is None:
+        return torch.empty_like(like) if like.is_contiguous() else like.new_empty(like.shape)
+    _same(name, t, like, like.shape)
+    _strided(p, name, t)
+    return t
+
+
+def _softmax_params(q, k, v, W, eps, causal):
     if q.dim() != 4 or k.dim() != 4 or not q.is_cuda or q.dtype not in _DTYPES:
         raise ValueError("q, k, v are [B,H,L,64] float32 or bfloat16 CUDA tensors")
     B, Hq, Lq, d = q.shape
-    Hk, Lk = k.shape[1], k.shape[2]
-    _same("as k", q, (B, Hk, Lk, d), k=k, v=v)
-    _aux("mask", mask, torch.uint8, (B, Lk), q.device)
-    _aux("q_pos", q_pos, torch.int32, (B,), q.device)
-    p = sa_softmax_params(B, Hq, Hk, Lq, Lk, d, min(int(W), 2**31 - 1), float(eps), int(bool(causal)),
-                          _DTYPES[q.dtype])
-    _strided(p, q=q, k=k, v=v)
+    shape = k.shape
+    if shape[0] != B or shape[3] != d:
+        raise ValueError(f"k: {tuple(shape)} does not go with q {tuple(q.shape)}")
+    _same("k", k, q, shape)
+    _same("v", v, q, shape)
+    p = sa_softmax_params(B, Hq, shape[1], Lq, shape[2], d, min(int(W), 2**31 - 1), float(eps),
+                          1 if causal else 0, _DTYPES[q.dtype])
+    _strided(p, "q", q)
+    _strided(p, "k", k)
+    _strided(p, "v", v)
     return p
 
 
@@ -712,10 +730,9 @@ def sinkhorn_attn_softmax_workspace_size(p: sa_softmax_params):
     return f.value, b.value
 
 
-def _softmax_ws(p, ws, which, device):
+def _softmax_ws(p, ws, which, like):
     if ws is None:
-        return torch.empty(sinkhorn_attn_softmax_workspace_size(p)[which], dtype=torch.uint8,
-                           device=device)
+        return like.new_empty(sinkhorn_attn_softmax_workspace_size(p)[which], dtype=torch.uint8)
     _contig(ws)
     return ws
 
@@ -730,21 +747,18 @@ def sinkhorn_attn_softmax_fwd(q, k, v, *, W, eps=1.0, causal=False, mask=None, q
     ``Lq``) and attends the keys within ``W`` positions (not the later ones when
     ``causal``); ``mask``: ``[B,Lk]`` uint8 (1 = valid) or None.  Returns ``(o, u)``:
     ``u`` is ``[B,Hq,Lq]`` float32, the row duals -log sum_j exp(S_ij)."""
-    p = _softmax_params(q, k, v, W, eps, causal, mask, q_pos)
-    dev = q.device
-    if o is None:
-        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    else:
-        _same("as q", q, q.shape, o=o)
-    _strided(p, o=o)
+    p = _softmax_params(q, k, v, W, eps, causal)
+    dev, B, Lk = q.device, p.B, p.Lk
+    pm = _aux("mask", mask, torch.uint8, (B, Lk), dev)
+    pp = _aux("q_pos", q_pos, torch.int32, (B,), dev)
+    o = _made("o", o, q, p)
+    rows = (B, p.Hq, p.Lq)
     if u is None:
-        u = torch.empty(q.shape[:3], dtype=torch.float32, device=dev)
-    else:
-        _aux("u", u, torch.float32, q.shape[:3], dev)
-    ws = _softmax_ws(p, ws, 0, dev)
-    _check(_on(dev, _L().sinkhorn_attn_softmax_fwd, ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v),
-               _ptr(mask), _ptr(q_pos), _ptr(o), _ptr(u), _ptr(ws), ws.numel(), _stream(dev)),
-           "sinkhorn_attn_softmax_fwd")
+        u = q.new_empty(rows, dtype=torch.float32)
+    ws = _softmax_ws(p, ws, 0, q)
+    _check(_on(dev, _L().sinkhorn_attn_softmax_fwd, ctypes.byref(p), q.data_ptr(), k.data_ptr(),
+               v.data_ptr(), pm, pp, o.data_ptr(), _aux("u", u, torch.float32, rows, dev),
+               ws.data_ptr(), ws.numel(), _raw_stream(dev)), "sinkhorn_attn_softmax_fwd")
     return o, u
 
 
@@ -753,23 +767,21 @@ def sinkhorn_attn_softmax_bwd(q, k, v, o, dO, u, *, W, eps=1.0, causal=False, ma
     """Backward of <dO, O> of :func:`sinkhorn_attn_softmax_fwd`, which recomputes
     the probabilities from the row duals ``u``.  Returns ``(dq, dk, dv)``, ``dk`` and
     ``dv`` summed over the query heads that share a key head."""
-    p = _softmax_params(q, k, v, W, eps, causal, mask, q_pos)
-    dev = q.device
-    _same("as q", q, q.shape, o=o, dO=dO)
-    _aux("u", u, torch.float32, q.shape[:3], dev)
-    if dq is None:
-        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    if dk is None:
-        dk = torch.empty(k.shape, dtype=k.dtype, device=dev)
-    if dv is None:
-        dv = torch.empty(k.shape, dtype=k.dtype, device=dev)
-    _same("as q", q, q.shape, dq=dq)
-    _same("as k", k, k.shape, dk=dk, dv=dv)
-    _strided(p, o=o, dO=dO, dq=dq, dk=dk, dv=dv)
-    ws = _softmax_ws(p, ws, 1, dev)
-    _check(_on(dev, _L().sinkhorn_attn_softmax_bwd, ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v),
-               _ptr(mask), _ptr(q_pos), _ptr(o), _ptr(dO), _ptr(u), _ptr(dq), _ptr(dk), _ptr(dv),
-               _ptr(ws), ws.numel(), _stream(dev)), "sinkhorn_attn_softmax_bwd")
+    p = _softmax_params(q, k, v, W, eps, causal)
+    dev, B = q.device, p.B
+    pm = _aux("mask", mask, torch.uint8, (B, p.Lk), dev)
+    pp = _aux("q_pos", q_pos, torch.int32, (B,), dev)
+    pu = _aux("u", u, torch.float32, (B, p.Hq, p.Lq), dev)
+    _same("o", o, q, q.shape)
+    _same("dO", dO, q, q.shape)
+    _strided(p, "o", o)
+    _strided(p, "dO", dO)
+    dq, dk, dv = _made("dq", dq, q, p), _made("dk", dk, k, p), _made("dv", dv, k, p)
+    ws = _softmax_ws(p, ws, 1, q)
+    _check(_on(dev, _L().sinkhorn_attn_softmax_bwd, ctypes.byref(p), q.data_ptr(), k.data_ptr(),
+               v.data_ptr(), pm, pp, o.data_ptr(), dO.data_ptr(), pu, dq.data_ptr(), dk.data_ptr(),
+               dv.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(dev)),
+           "sinkhorn_attn_softmax_bwd")
     return dq, dk, dv
 
 
@@ -793,29 +805,22 @@ def _rotary(entry, q, k, freqs, pos, interleaved, scale, q_out, k_out):
     if q.dim() != 4 or not q.is_cuda or q.dtype not in _DTYPES:
         raise ValueError("q, k are [B,H,L,d] float32 or bfloat16 CUDA tensors")
     B, Hq, L, d = q.shape
-    dev, Hk = q.device, 0
+    dev, Hk, pk, pko = q.device, 0, None, None
     if k is not None:
-        if k.dim() != 4:
-            raise ValueError("q, k are [B,H,L,d] float32 or bfloat16 CUDA tensors")
-        Hk = k.shape[1]
-        _same("as q, but for the heads", q, (B, Hk, L, d), k=k)
-    _aux("freqs", freqs, torch.float64, (freqs.numel(),), dev)
-    _aux("pos", pos, torch.int32, (B, L), dev)
-    p = sa_rotary_params(B, Hq, Hk, L, d, 2 * freqs.numel(), int(bool(interleaved)), float(scale),
+        Hk = k.shape[1] if k.dim() == 4 else 0
+        _same("k", k, q, (B, Hk, L, d))
+    pf = _aux("freqs", freqs, torch.float64, (freqs.numel(),), dev)
+    pp = _aux("pos", pos, torch.int32, (B, L), dev)
+    p = sa_rotary_params(B, Hq, Hk, L, d, 2 * freqs.numel(), 1 if interleaved else 0, float(scale),
                          _DTYPES[q.dtype])
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    else:
-        _same("as q", q, q.shape, q_out=q_out)
-    _strided(p, q=q, q_out=q_out)
+    _strided(p, "q", q)
+    q_out = _made("q_out", q_out, q, p)
     if k is not None:
-        if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-        else:
-            _same("as k", k, k.shape, k_out=k_out)
-        _strided(p, k=k, k_out=k_out)
-    _check(_on(dev, getattr(_L(), entry), ctypes.byref(p), _ptr(freqs), _ptr(pos), _ptr(q), _ptr(k),
-               _ptr(q_out), _ptr(k_out if k is not None else None), _stream(dev)), entry)
+        _strided(p, "k", k)
+        k_out = _made("k_out", k_out, k, p)
+        pk, pko = k.data_ptr(), k_out.data_ptr()
+    _check(_on(dev, getattr(_L(), entry), ctypes.byref(p), pf, pp, q.data_ptr(), pk,
+               q_out.data_ptr(), pko, _raw_stream(dev)), entry)
     return q_out, (k_out if k is not None else None)
 
 

@@ -141,9 +141,9 @@ def test_python_checks():
         sa.sinkhorn_attn_rotary_fwd(q, q, torch.zeros(32, dtype=torch.float64))
     p = P()
     with pytest.raises(ValueError):  # an expanded tensor is never taken for a contiguous one
-        sa._strided(p, q=torch.zeros(1, 1, 1, 64).expand(2, 4, 50, 64))
+        sa._strided(p, "q", torch.zeros(1, 1, 1, 64).expand(2, 4, 50, 64))
     with pytest.raises(ValueError):
-        sa._strided(p, q=torch.zeros(2, 4, 64, 50).transpose(2, 3))
+        sa._strided(p, "q", torch.zeros(2, 4, 64, 50).transpose(2, 3))
 
 
 # ------------------------------------------------------------------ the float64 forms

@@ -215,7 +215,7 @@ def test_workspace_status_and_reuse():
     import banded_log_domain_b200 as sa
 
     q, k, v, dO = draw(BF16, 1, 2, 2, 1, 9000, seed=3)
-    p = sa._softmax_params(q, k, v, 9000, 1.0, True, None, None)
+    p = sa._softmax_params(q, k, v, 9000, 1.0, True)
     f, b = sa.sinkhorn_attn_softmax_workspace_size(p)
     ws = torch.full((max(f, b),), 0x5a, dtype=torch.uint8, device="cuda")  # needs no initialisation
     kw = dict(W=9000, causal=True)
