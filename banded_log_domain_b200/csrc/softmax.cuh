@@ -26,6 +26,7 @@ struct Args {
     float c, c2;          // 1 / (sqrt(d) eps), and that times log2(e)
     const int* q_pos;     // [B], or NULL: Lk - Lq
     const uint8_t* mask;  // [B][Lk], or NULL
+    int2* span;           // [B]: first and last unmasked token, with a mask
     View q, k, v, o, dO, dq, dk, dv;
     float* u;             // [B][Hq][Lq]
     float* D;             // [B][Hq][Lq], backward
@@ -50,18 +51,51 @@ struct Args {
     }
 };
 
-// The keys [lo, hi] that any of queries i0 .. i1 (inclusive) may attend; empty
-// (hi < lo) when all lie outside the sequence.
-__device__ __forceinline__ void tile_keys(const Args& a, long long first, int i0, int i1, int& lo, int& hi) {
-    long long p0 = first + i0, p1 = first + i1;
-    if (p0 < 0) p0 = 0;
-    if (p1 > a.Lk - 1) p1 = a.Lk - 1;
+// Sequence b's tokens [x, y] outside of which all are masked.
+__device__ __forceinline__ int2 span(const Args& a, int b) {
+    return a.mask ? a.span[b] : make_int2(0, a.Lk - 1);
+}
+
+// The keys [lo, hi] that any of queries i0 .. i1 (inclusive) of sequence b may
+// attend; empty (hi < lo) when none may.
+__device__ __forceinline__ void tile_keys(const Args& a, int b, int i0, int i1, int& lo, int& hi) {
+    const int2 s = span(a, b);
+    long long p0 = a.first(b) + i0, p1 = a.first(b) + i1;
+    if (p0 < s.x) p0 = s.x;
+    if (p1 > s.y) p1 = s.y;
     lo = 0;
     hi = -1;
     if (p1 < p0) return;
     int x;
     a.keys(p0, lo, x);
     a.keys(p1, x, hi);
+    lo = max(lo, s.x);
+    hi = min(hi, s.y);
+}
+
+// The spans, one block per sequence: padding at either end then costs no tiles.
+__global__ void __launch_bounds__(1024) k_span(const Args a) {
+    __shared__ int lo[32], hi[32];
+    const uint8_t* m = a.mask + (long long)blockIdx.x * a.Lk;
+    int x = 0x7fffffff, y = -1;
+#pragma unroll 8
+    for (int j = threadIdx.x; j < a.Lk; j += 1024)
+        if (m[j]) {
+            x = min(x, j);
+            y = j;
+        }
+    x = __reduce_min_sync(~0u, x);
+    y = __reduce_max_sync(~0u, y);
+    if ((threadIdx.x & 31) == 0) {
+        lo[threadIdx.x >> 5] = x;
+        hi[threadIdx.x >> 5] = y;
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        x = __reduce_min_sync(~0u, lo[threadIdx.x]);
+        y = __reduce_max_sync(~0u, hi[threadIdx.x]);
+        if (threadIdx.x == 0) a.span[blockIdx.x] = make_int2(y < 0 ? 0 : x, y);
+    }
 }
 
 // Joins the parts of split rows: o = sum_s 2^(m_s - m) o_s / l, one warp per row,

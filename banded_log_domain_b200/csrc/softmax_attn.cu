@@ -9,6 +9,7 @@
 #include "softmax_simt.cuh"
 #include "softmax_tc.cuh"
 #include "softmax_tc_bwd.cuh"
+#include "softmax_token.cuh"
 
 namespace sa {
 namespace {
@@ -21,8 +22,9 @@ constexpr int kMaxGroup = 64;   // query heads per key head (they share a tile's
 struct Plan {
     bool tc;
     int G, nq, nr, per, ntile, nktile, nsplit, nparts;
+    int token;  // blocks of the single-token forward, 0 where it does not apply
     long long rows;  // B * Hq * Lq
-    size_t fwd_bytes, bwd_bytes, part_ml;
+    size_t fwd_bytes, bwd_bytes, part_ml, span;  // span: in either workspace
 };
 
 sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
@@ -62,10 +64,21 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     if (tiles > 0 && tiles < sms)
         pl->nsplit = (int)std::max<long long>(1, std::min(2LL * sms / tiles, chunks / (pl->tc ? 8 : 4)));
     pl->nparts = pl->nsplit;
-    const long long parts = pl->nparts > 1 ? pl->rows * pl->nparts : 0;
-    pl->part_ml = kHeader + align_up((size_t)parts * kD * 4);
+    long long parts = pl->nparts > 1 ? pl->rows * pl->nparts : 0;
+    // Few query rows per key head are bound by reading the keys and
+    // values: a kernel without tiles, whose blocks (two per SM, of two chunks or
+    // more) share all sequences' chunks evenly, takes 48 us where the tiled forward
+    // takes 83 (8 sequences of 16384 to 32768 tokens, 4 heads to a key head, bf16).
+    pl->token = 0;
+    if ((long long)pl->G * p->Lq <= sm::token::max_rows(pl->tc) && p->B <= sm::token::MAXB && BH <= 4096 && BH > 0) {
+        pl->token = (int)std::max<long long>(1, std::min<long long>(2LL * sms, BH * chunks / 2));
+        parts = (pl->token + BH) * pl->G * p->Lq;
+    }
+    pl->span = kHeader;
+    const size_t head = kHeader + align_up((size_t)p->B * 8);
+    pl->part_ml = head + align_up((size_t)parts * kD * 4);
     pl->fwd_bytes = pl->part_ml + align_up((size_t)parts * 8);
-    pl->bwd_bytes = kHeader + align_up((size_t)pl->rows * 4);
+    pl->bwd_bytes = head + align_up((size_t)pl->rows * 4);
     return SA_OK;
 }
 
@@ -114,6 +127,7 @@ void base_args(sm::Args* a, const sa_softmax_params* p, const Plan& pl, const ui
     a->q_pos = q_pos;
     a->mask = mask;
     a->status = (int*)ws;
+    a->span = (int2*)((char*)ws + pl.span);
     a->nq = pl.nq;
     a->ntile = pl.ntile;
     a->nsplit = 1;
@@ -157,7 +171,26 @@ cudaError_t fwd_tc(const sa_softmax_params* p, const Plan& pl, const sm::Args& a
     return e;
 }
 
+cudaError_t fwd_token(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
+    using namespace sm::token;
+    const int rows = pl.G * p->Lq;
+    // both launched with programmatic stream serialisation (they wait for what
+    // runs before them), so that the second's launch hides behind the first
+    auto go = [&](auto kern, int threads, int smem) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        return e != cudaSuccess ? e : launch_pdl(kern, dim3(pl.token), dim3(threads), smem, st, a);
+    };
+    const cudaError_t e = pl.tc ? go(rows <= 8 ? mma::k_token<1> : mma::k_token<2>, THREADS_MMA, mma::SMEM)
+                                : go(rows == 1   ? k_token<1>
+                                     : rows == 2 ? k_token<2>
+                                                 : k_token<4>, THREADS, SMEM);
+    if (e != cudaSuccess || (pl.token == 1 && !a.q_pos && !a.mask)) return e;
+    const dim3 grid((unsigned)(((long long)p->B * p->Hk * rows + 3) / 4));
+    return launch_pdl(pl.tc ? k_token_join<__nv_bfloat16> : k_token_join<float>, grid, dim3(128), 0, st, a, pl.token);
+}
+
 cudaError_t fwd_launch(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
+    if (pl.token) return fwd_token(p, pl, a, st);
     const cudaError_t e = !pl.tc       ? fwd_simt(p, pl, a, st)
                           : pl.nr == 4 ? fwd_tc<4>(p, pl, a, st)
                           : pl.nr == 2 ? fwd_tc<2>(p, pl, a, st)
@@ -249,10 +282,11 @@ sa_status sinkhorn_attn_softmax_fwd(const sa_softmax_params* p, const void* q, c
     a.u = u;
     a.nsplit = pl.nsplit;
     a.nparts = pl.nparts;
-    a.part_o = (float*)((char*)ws + kHeader);
+    a.part_o = (float*)((char*)ws + kHeader + align_up((size_t)p->B * 8));
     a.part_ml = (float2*)((char*)ws + pl.part_ml);
     const cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = fwd_launch(p, pl, a, st);
+    cudaError_t e = mask ? launch(sm::k_span, p->B, 1024, 0, st, a) : cudaSuccess;
+    if (e == cudaSuccess) e = fwd_launch(p, pl, a, st);
     return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 
@@ -282,13 +316,14 @@ sa_status sinkhorn_attn_softmax_bwd(const sa_softmax_params* p, const void* q, c
     if (pl.rows > 0 && (!device_ok(q) || !device_ok(o) || !device_ok(dO) || !device_ok(u) || !device_ok(dq)))
         return SA_ERR_INVALID_ARG;
     a.u = const_cast<float*>(u);
-    a.D = (float*)((char*)ws + kHeader);
+    a.D = (float*)((char*)ws + kHeader + align_up((size_t)p->B * 8));
     // With few keys a row's probabilities are large and dO . O, taken from the
     // rounded O, is off by about as much as the dS it is subtracted in: up to
     // 64 keys the sweep forms D itself, in a pass of its own over them.
     a.exact_d = p->dtype == SA_BF16 && (long long)a.W + a.R + 1 <= 64;
     const cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = pl.rows > 0 ? bwd_launch(p, pl, a, st) : zero_grads(p, a, st);
+    cudaError_t e = mask && pl.rows > 0 ? launch(sm::k_span, p->B, 1024, 0, st, a) : cudaSuccess;
+    if (e == cudaSuccess) e = pl.rows > 0 ? bwd_launch(p, pl, a, st) : zero_grads(p, a, st);
     return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 

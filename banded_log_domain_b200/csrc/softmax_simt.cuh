@@ -117,7 +117,7 @@ struct RowTile {
         b = x / a.Hk;
         i0 = qt * a.nq;
         first = a.first(b);
-        tile_keys(a, first, i0, min(i0 + a.nq, a.Lq) - 1, jlo, jhi);
+        tile_keys(a, b, i0, min(i0 + a.nq, a.Lq) - 1, jlo, jhi);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             int h, t;
@@ -335,12 +335,13 @@ __global__ void __launch_bounds__(THREADS) k_bwd_kv(const Args a) {
     x /= a.ntile;
     const int hk = x % a.Hk, b = x / a.Hk;
     const long long first = a.first(b);
-    // queries whose position lies in [j0 - R, j0 + 63 + W] and in the sequence
-    const long long pl = j0 - (long long)a.R > 0 ? j0 - (long long)a.R : 0;
-    const long long ph = (long long)j0 + 63 + a.W < a.Lk - 1 ? (long long)j0 + 63 + a.W : a.Lk - 1;
+    // queries whose position lies in [j0 - R, j0 + 63 + W] and in the span
+    const int2 sp = span(a, b);
+    const long long pl = j0 - (long long)a.R > sp.x ? j0 - (long long)a.R : sp.x;
+    const long long ph = (long long)j0 + 63 + a.W < sp.y ? (long long)j0 + 63 + a.W : sp.y;
     const long long il = pl - first > 0 ? pl - first : 0;
     const long long ih = ph - first < a.Lq - 1 ? ph - first : a.Lq - 1;
-    const int n = ih < il ? 0 : (int)((ih - il) / 64 + 1);
+    const int n = ih < il || j0 > sp.y || j0 + 63 < sp.x ? 0 : (int)((ih - il) / 64 + 1);
     auto krow = [&](const View& y, int r) -> const T* {
         const int j = j0 + r;
         return j < a.Lk && a.live(b, j) ? y.at<T>(b, hk, j) : nullptr;

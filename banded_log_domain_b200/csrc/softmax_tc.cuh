@@ -182,7 +182,7 @@ __device__ __forceinline__ void make_item(const Args& a, int idx, Item& w) {
         const int i = w.i0 + t * a.nq;
         lo[t] = 0;
         hi[t] = -1;
-        if (i < a.Lq) tile_keys(a, w.first, i, min(i + a.nq, a.Lq) - 1, lo[t], hi[t]);
+        if (i < a.Lq) tile_keys(a, w.b, i, min(i + a.nq, a.Lq) - 1, lo[t], hi[t]);
         if (hi[t] >= lo[t]) {
             vlo = vhi < vlo ? lo[t] : min(vlo, lo[t]);
             vhi = max(vhi, hi[t]);
@@ -334,17 +334,12 @@ __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_
                     if ((bits[0] & bits[1]) != ~0u) {
                         uint8_t* v = sm + Y::ST + s * 2 * KT + KT;
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            uint32_t off = ~bits[k];
-                            while (off) {  // four rows at a time, eight lanes of 16 bytes each
-                                uint32_t m = off;
-                                for (int x = 0; x < (lane >> 3); ++x) m &= m - 1;
-                                if (m)
-                                    *reinterpret_cast<uint4*>(v + (32 * k + __ffs(m) - 1) * 128 + (lane & 7) * 16) =
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)  // four rows at a time, eight lanes of 16 bytes each
+                                if (!((bits[k] >> (4 * e + (lane >> 3))) & 1u))
+                                    *reinterpret_cast<uint4*>(v + (32 * k + 4 * e + (lane >> 3)) * 128 + (lane & 7) * 16) =
                                         make_uint4(0, 0, 0, 0);
-                                for (int x = 0; x < 4; ++x) off &= off - 1;
-                            }
-                        }
                         tc::fence_async_smem();
                     }
                     __syncwarp();

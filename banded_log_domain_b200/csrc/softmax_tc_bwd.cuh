@@ -68,12 +68,14 @@ __device__ __forceinline__ void make_item(const Args& a, int idx, Item& w) {
     int lo = 0, hi = -1;
     if (MODE == DQ) {  // the later the query, the more keys a causal band holds
         w.r0 = (a.ntile - 1 - rt) * a.nq;
-        tile_keys(a, w.first, w.r0, min(w.r0 + a.nq, a.Lq) - 1, lo, hi);
-    } else {  // queries whose position lies in [r0 - R, r0 + 127 + W], and in the sequence
+        tile_keys(a, w.b, w.r0, min(w.r0 + a.nq, a.Lq) - 1, lo, hi);
+    } else {  // queries whose position lies in [k0 - R, k1 + W], and in the span
         w.r0 = rt * 128;
-        long long p0 = (long long)w.r0 - a.R, p1 = (long long)min(w.r0 + 127, a.Lk - 1) + a.W;
-        p0 = p0 > 0 ? p0 : 0;
-        p1 = p1 < a.Lk - 1 ? p1 : a.Lk - 1;
+        const int2 s = span(a, w.b);
+        const int k0 = max(w.r0, s.x), k1 = min(w.r0 + 127, s.y);
+        long long p0 = (long long)k0 - a.R, p1 = (long long)k1 + a.W;
+        p0 = p0 > s.x ? p0 : s.x;
+        p1 = k1 < k0 ? -1 : p1 < s.y ? p1 : s.y;
         p0 -= w.first;
         p1 -= w.first;
         if (p0 < 0) p0 = 0;
@@ -246,19 +248,15 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                         if ((bits[0] & bits[1]) != ~0u) {
                             uint8_t* x = sm + OFF_ST + s * 2 * KT;
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                uint32_t off = ~bits[k];
-                                while (off) {  // four rows at a time, eight lanes of 16 bytes each
-                                    uint32_t m = off;
-                                    for (int z = 0; z < (lane >> 3); ++z) m &= m - 1;
-                                    if (m) {
-                                        uint4* q = reinterpret_cast<uint4*>(x + (32 * k + __ffs(m) - 1) * 128 + (lane & 7) * 16);
+                            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)  // four rows at a time, eight lanes of 16 bytes each
+                                    if (!((bits[k] >> (4 * e + (lane >> 3))) & 1u)) {
+                                        uint4* q = reinterpret_cast<uint4*>(x + (32 * k + 4 * e + (lane >> 3)) * 128 +
+                                                                            (lane & 7) * 16);
                                         q[0] = make_uint4(0, 0, 0, 0);
                                         if (MODE == DKV) q[KT / 16] = make_uint4(0, 0, 0, 0);
                                     }
-                                    for (int z = 0; z < 4; ++z) off &= off - 1;
-                                }
-                            }
                             tc::fence_async_smem();
                         }
                         __syncwarp();

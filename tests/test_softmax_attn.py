@@ -38,7 +38,7 @@ def test_null_params_small_workspace_and_host_pointers():
     assert lib.sinkhorn_attn_softmax_bwd(None, *[None] * 12, 1 << 40, None) == -1
     p = P()
     f, b = sa.sinkhorn_attn_softmax_workspace_size(p)
-    assert b == 256 + (2 * 4 * 50 * 4 + 255) // 256 * 256
+    assert b == 512 + (2 * 4 * 50 * 4 + 255) // 256 * 256  # status, spans, D
     assert lib.sinkhorn_attn_softmax_fwd(ctypes.byref(p), *[None] * 8, f - 1, None) == -3
     assert lib.sinkhorn_attn_softmax_bwd(ctypes.byref(p), *[None] * 12, b - 1, None) == -3
     assert lib.sinkhorn_attn_softmax_fwd(ctypes.byref(p), *[None] * 8, f, None) == -1
@@ -56,7 +56,7 @@ def test_empty_problems_succeed():
         f, b = sa.sinkhorn_attn_softmax_workspace_size(p)
         assert lib.sinkhorn_attn_softmax_fwd(ctypes.byref(p), *[None] * 8, f, None) == 0
         assert lib.sinkhorn_attn_softmax_bwd(ctypes.byref(p), *[None] * 12, b, None) == 0
-    assert lib.sinkhorn_attn_softmax_fwd(ctypes.byref(P(Lq=0)), *[None] * 8, 256, None) == 0
+    assert lib.sinkhorn_attn_softmax_fwd(ctypes.byref(P(Lq=0)), *[None] * 8, 512, None) == 0
 
 
 @pytest.mark.parametrize("stride", [(-6400, 640, 64), (6400, 0, 64), (6400, 640, 60), (1 << 39, 640, 64)])
@@ -77,7 +77,7 @@ def test_workspace_is_bounded_and_grows_with_the_rows_only():
             f, _ = sa.sinkhorn_attn_softmax_workspace_size(P(B=B, Hq=64, Hk=1, Lq=1, Lk=Lk, W=Lk))
             assert f <= 37 << 20
     f, b = sa.sinkhorn_attn_softmax_workspace_size(P(B=1, Hq=16, Hk=16, Lq=32768, Lk=32768, W=256))
-    assert f == 256 and b == 256 + 16 * 32768 * 4
+    assert f == 512 and b == 512 + 16 * 32768 * 4
 
 
 @pytest.mark.parametrize("kw,status", [
