@@ -21,7 +21,7 @@ constexpr int kMaxGroup = 64;   // query heads per key head (they share a tile's
 // queries) to a forward item, its keys in `nsplit` parts.
 struct Plan {
     bool tc;
-    int G, nq, nr, per, ntile, nktile, nsplit, nparts;
+    int G, nq, rpt, nr, per, ntile, nktile, nsplit, nparts;
     int token;  // blocks of the single-token forward, 0 where it does not apply
     long long rows;  // B * Hq * Lq
     size_t fwd_bytes, bwd_bytes, part_ml, span;  // span: in either workspace
@@ -44,14 +44,17 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     pl->rows = (long long)p->B * p->Hq * p->Lq;
     pl->tc = p->dtype == SA_BF16;
     const int sms = sm_count();
-    pl->nq = (pl->tc ? 128 : 64) / pl->G;
-    const long long BH = (long long)p->B * p->Hk, RT = (p->Lq + pl->nq - 1) / pl->nq;  // row tiles
+    const long long BH = (long long)p->B * p->Hk;
+    // fp32 tiles of 64 rows, or of 16 where those would leave SMs without one
+    pl->rpt = pl->G <= 16 && BH * ((p->Lq + 64 / pl->G - 1) / (64 / pl->G)) < sms ? 1 : 4;
+    pl->nq = (pl->tc ? 128 : 16 * pl->rpt) / pl->G;
+    const long long RT = (p->Lq + pl->nq - 1) / pl->nq;  // row tiles
     // The tensor-core forward's items are 4, 2 or 1 row tiles (see softmax_tc.cuh).
     pl->nr = 1;
     if (pl->tc && RT > 1) pl->nr = BH * ((RT + 3) / 4) >= 4LL * sms ? 4 : 2;
     pl->per = pl->nr * pl->nq;
     pl->ntile = (int)((RT + pl->nr - 1) / pl->nr);
-    pl->nktile = (p->Lk + 63) / 64;
+    pl->nktile = (p->Lk + 16 * pl->rpt - 1) / (16 * pl->rpt);
     const long long tiles = BH * pl->ntile;
     if (std::max(tiles, BH * pl->nktile) > (1LL << 30)) return SA_ERR_UNSUPPORTED;
     // A few query rows over many keys (single new tokens) would leave most SMs
@@ -135,9 +138,11 @@ void base_args(sm::Args* a, const sa_softmax_params* p, const Plan& pl, const ui
     a->exact_d = 0;
 }
 
+template <int RPT>
 cudaError_t fwd_simt(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
     const long long tiles = (long long)p->B * p->Hk * pl.ntile;
-    return launch(sm::simt::k_fwd<float>, tiles * pl.nsplit, sm::simt::THREADS, sm::simt::smem_bytes(4), st, a);
+    return launch(sm::simt::k_fwd<float, RPT>, tiles * pl.nsplit, sm::simt::THREADS, sm::simt::smem_bytes(RPT, 2, 2), st,
+                  a);
 }
 
 // A [B][H][L][64] bf16 view as a 4-D tensor; boxes of `tokens` x `heads` rows.
@@ -191,7 +196,7 @@ cudaError_t fwd_token(const sa_softmax_params* p, const Plan& pl, const sm::Args
 
 cudaError_t fwd_launch(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
     if (pl.token) return fwd_token(p, pl, a, st);
-    const cudaError_t e = !pl.tc       ? fwd_simt(p, pl, a, st)
+    const cudaError_t e = !pl.tc         ? (pl.rpt == 4 ? fwd_simt<4>(p, pl, a, st) : fwd_simt<1>(p, pl, a, st))
                           : pl.nr == 4 ? fwd_tc<4>(p, pl, a, st)
                           : pl.nr == 2 ? fwd_tc<2>(p, pl, a, st)
                                        : fwd_tc<1>(p, pl, a, st);
@@ -199,17 +204,14 @@ cudaError_t fwd_launch(const sa_softmax_params* p, const Plan& pl, const sm::Arg
     return launch(pl.tc ? sm::k_join<__nv_bfloat16> : sm::k_join<float>, (pl.rows + 3) / 4, 128, 0, st, a);
 }
 
+template <int RPT>
 cudaError_t bwd_simt(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cudaStream_t st) {
+    using namespace sm::simt;
     const long long BH = (long long)p->B * p->Hk;
-    a.nq = 64 / pl.G;
-    a.ntile = (p->Lq + a.nq - 1) / a.nq;
-    if (pl.rows > 0) {
-        const cudaError_t e =
-            launch(sm::simt::k_bwd_q<float>, BH * a.ntile, sm::simt::THREADS, sm::simt::smem_bytes(5), st, a);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = launch(k_bwd_q<float, RPT>, BH * a.ntile, THREADS, smem_bytes(RPT, 3, 2), st, a);
+    if (e != cudaSuccess) return e;
     a.ntile = pl.nktile;
-    return launch(sm::simt::k_bwd_kv<float>, BH * pl.nktile, sm::simt::THREADS, sm::simt::smem_bytes(6), st, a);
+    return launch(k_bwd_kv<float, RPT>, BH * pl.nktile, THREADS, smem_bytes(RPT, 4, 2), st, a);
 }
 
 template <int MODE, bool EXACT>
@@ -238,7 +240,7 @@ cudaError_t zero_grads(const sa_softmax_params* p, sm::Args& a, cudaStream_t st)
 }
 
 cudaError_t bwd_launch(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cudaStream_t st) {
-    if (!pl.tc) return bwd_simt(p, pl, a, st);
+    if (!pl.tc) return pl.rpt == 4 ? bwd_simt<4>(p, pl, a, st) : bwd_simt<1>(p, pl, a, st);
     const long long BH = (long long)p->B * p->Hk;
     a.nq = pl.nq;
     a.ntile = (p->Lq + a.nq - 1) / a.nq;

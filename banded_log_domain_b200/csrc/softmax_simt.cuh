@@ -1,6 +1,8 @@
-// Softmax attention on the FP32 pipe: 64 x 64 tiles, 256 threads of 4 x 4
-// entries.  All products are packed f32x2 FMAs on operands in shared memory.
-// Bound by FFMA issue and the shared-memory reads that feed it.
+// Softmax attention on the FP32 pipe (fp32 storage): tiles of 16 RPT rows x 64
+// columns, 256 threads of RPT x 4 entries.  All products are packed f32x2 FMAs on
+// operands in shared memory; bound by FFMA issue and the shared-memory reads that
+// feed it.  RPT is 4; 1 where tiles of 64 rows would leave SMs without one (the
+// 512-token problem's three kernels: 100 -> 40 us).
 #pragma once
 
 #include "softmax.cuh"
@@ -11,27 +13,31 @@ namespace sm {
 namespace simt {
 
 constexpr int LD = 68;            // floats per tile row: 16-byte aligned, rows 4 banks apart
-constexpr int TILE = 64 * LD;     // floats of a 64 x 64 tile
 constexpr int THREADS = 256;
 
-__host__ __device__ constexpr int smem_bytes(int tiles) { return tiles * TILE * 4; }
+// floats of tiles of 16 RPT rows and of the 64-row tiles of a chunk
+constexpr int TILE = 64 * LD;
+__host__ __device__ constexpr int rtile(int rpt) { return 16 * rpt * LD; }
+// bytes of `r` row tiles and `c` chunk tiles
+__host__ __device__ constexpr int smem_bytes(int rpt, int r, int c) { return (r * rtile(rpt) + c * TILE) * 4; }
 
-// acc[i][j] += sum_k A[ty * 4 + i][k] B[tx + 16 j][k] (k pairs summed apart, then together)
-__device__ __forceinline__ void mm_abt(const float* A, const float* B, int ty, int tx, float (&s)[4][4]) {
-    uint64_t acc[4][4];
+// s[i][j] = sum_k A[ty * RPT + i][k] B[tx + 16 j][k] (even and odd k apart, then together)
+template <int RPT>
+__device__ __forceinline__ void mm_abt(const float* A, const float* B, int ty, int tx, float (&s)[RPT][4]) {
+    uint64_t acc[RPT][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RPT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0;
 #pragma unroll 4
     for (int k = 0; k < 64; k += 4) {
-        ulonglong2 x[4], y[4];
+        ulonglong2 x[RPT], y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const ulonglong2*>(A + (ty * 4 + i) * LD + k);
+        for (int i = 0; i < RPT; ++i) x[i] = *reinterpret_cast<const ulonglong2*>(A + (ty * RPT + i) * LD + k);
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const ulonglong2*>(B + (tx + 16 * j) * LD + k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RPT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 acc[i][j] = tc::fma2(x[i].x, y[j].x, acc[i][j]);
@@ -39,7 +45,7 @@ __device__ __forceinline__ void mm_abt(const float* A, const float* B, int ty, i
             }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RPT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float lo, hi;
@@ -48,18 +54,19 @@ __device__ __forceinline__ void mm_abt(const float* A, const float* B, int ty, i
         }
 }
 
-// acc[i][0..3] (two packed pairs) += sum_j P[ty * 4 + i][j] X[j][tx * 4 ..]
-__device__ __forceinline__ void mm_ab(const float* P, const float* X, int ty, int tx, uint64_t (&acc)[4][2]) {
+// acc[i] (two packed pairs) += sum_j P[ty * RPT + i][j] X[j][tx * 4 ..]
+template <int RPT>
+__device__ __forceinline__ void mm_ab(const float* P, const float* X, int ty, int tx, uint64_t (&acc)[RPT][2]) {
 #pragma unroll 4
     for (int j = 0; j < 64; j += 4) {
-        float4 p[4];
+        float4 p[RPT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(P + (ty * 4 + i) * LD + j);
+        for (int i = 0; i < RPT; ++i) p[i] = *reinterpret_cast<const float4*>(P + (ty * RPT + i) * LD + j);
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
             const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(X + (j + jj) * LD + tx * 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < RPT; ++i) {
                 const float e = reinterpret_cast<const float*>(&p[i])[jj];
                 const uint64_t ee = tc::pk2(e, e);
                 acc[i][0] = tc::fma2(ee, x.x, acc[i][0]);
@@ -69,12 +76,12 @@ __device__ __forceinline__ void mm_ab(const float* P, const float* X, int ty, in
     }
 }
 
-// One 64 x 64 tile of rows base(r) (nullptr: zeros) into shared memory as float.
-template <typename T, typename F>
+// A tile of ROWS rows base(r) (nullptr: zeros) into shared memory.
+template <typename T, int ROWS, typename F>
 __device__ __forceinline__ void load_tile(float* dst, F base) {
     constexpr int V = 16 / sizeof(T), PER = 64 / V;
 #pragma unroll
-    for (int x = threadIdx.x; x < 64 * PER; x += THREADS) {
+    for (int x = threadIdx.x; x < ROWS * PER; x += THREADS) {
         const int r = x / PER, c = (x % PER) * V;
         const T* p = base(r);
         float e[V];
@@ -101,10 +108,11 @@ __device__ __forceinline__ float max16(float x) {
 }
 
 // A tile of query rows: which query and head a row is, and the keys it attends.
+template <int RPT>
 struct RowTile {
     int b, hk, i0, part;
     long long first;
-    int lo[4], hi[4];  // this thread's four rows (hi < lo: none)
+    int lo[RPT], hi[RPT];  // this thread's rows (hi < lo: none)
     int jlo, jhi;      // the tile's keys
 
     __device__ void init(const Args& a, int ty) {
@@ -119,11 +127,11 @@ struct RowTile {
         first = a.first(b);
         tile_keys(a, b, i0, min(i0 + a.nq, a.Lq) - 1, jlo, jhi);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < RPT; ++i) {
             int h, t;
             lo[i] = 0;
             hi[i] = -1;
-            if (!row(a, ty * 4 + i, h, t)) continue;
+            if (!row(a, ty * RPT + i, h, t)) continue;
             const long long p = first + t;
             if (p >= 0 && p < a.Lk && a.live(b, (int)p)) a.keys(p, lo[i], hi[i]);
         }
@@ -148,25 +156,25 @@ __device__ __forceinline__ void live_keys(const Args& a, int b, int c0, uint32_t
 __device__ __forceinline__ bool live_bit(const uint32_t* words, int j) { return (words[j >> 5] >> (j & 31)) & 1u; }
 
 // One pass over the keys with the running maximum and sum of each row.
-template <typename T>
-__global__ void __launch_bounds__(THREADS) k_fwd(const Args a) {
+template <typename T, int RPT>
+__global__ void __launch_bounds__(THREADS, 2) k_fwd(const Args a) {
     extern __shared__ __align__(16) float sh[];
     __shared__ uint32_t words[2];
-    float *Q = sh, *K = Q + TILE, *V = K + TILE, *P = V + TILE;
+    float *Q = sh, *P = Q + rtile(RPT), *K = P + rtile(RPT), *V = K + TILE;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
-    RowTile rt;
+    RowTile<RPT> rt;
     rt.init(a, ty);
     const int n = (rt.jhi - rt.jlo + 64) / 64;  // 0 when empty
     const int n0 = (int)((long long)n * rt.part / a.nsplit), n1 = (int)((long long)n * (rt.part + 1) / a.nsplit);
-    load_tile<T>(Q, [&](int r) -> const T* {
+    load_tile<T, 16 * RPT>(Q, [&](int r) -> const T* {
         int h, t;
         return rt.row(a, r, h, t) ? a.q.at<T>(rt.b, h, t) : nullptr;
     });
-    float m[4], l[4];
-    uint64_t o[4][2];
+    float m[RPT], l[RPT];
+    uint64_t o[RPT][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RPT; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
         o[i][0] = o[i][1] = 0;
@@ -179,13 +187,13 @@ __global__ void __launch_bounds__(THREADS) k_fwd(const Args a) {
             const int j = c0 + r;
             return j <= rt.jhi && a.live(rt.b, j) ? x.at<T>(rt.b, rt.hk, j) : nullptr;
         };
-        load_tile<T>(K, [&](int r) { return row(a.k, r); });
-        load_tile<T>(V, [&](int r) { return row(a.v, r); });
+        load_tile<T, 64>(K, [&](int r) { return row(a.k, r); });
+        load_tile<T, 64>(V, [&](int r) { return row(a.v, r); });
         __syncthreads();
-        float s[4][4];
-        mm_abt(Q, K, ty, tx, s);
+        float s[RPT][4];
+        mm_abt<RPT>(Q, K, ty, tx, s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < RPT; ++i) {
             float top = m[i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -203,7 +211,7 @@ __global__ void __launch_bounds__(THREADS) k_fwd(const Args a) {
             for (int j = 0; j < 4; ++j) {
                 const float p = ex2(s[i][j] - use);
                 add += p;
-                P[(ty * 4 + i) * LD + tx + 16 * j] = p;
+                P[(ty * RPT + i) * LD + tx + 16 * j] = p;
             }
             l[i] = l[i] * f + add;  // this thread's share of the sum
             const uint64_t ff = tc::pk2(f, f);
@@ -211,13 +219,13 @@ __global__ void __launch_bounds__(THREADS) k_fwd(const Args a) {
             o[i][1] = tc::fma2(o[i][1], ff, 0);
         }
         __syncwarp();  // a warp writes and reads the same rows of P
-        mm_ab(P, V, ty, tx, o);
+        mm_ab<RPT>(P, V, ty, tx, o);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RPT; ++i) {
         const float total = sum16(l[i]);
         int h, t;
-        if (!rt.row(a, ty * 4 + i, h, t)) continue;
+        if (!rt.row(a, ty * RPT + i, h, t)) continue;
         float x[4];
         tc::upk2(o[i][0], x[0], x[1]);
         tc::upk2(o[i][1], x[2], x[3]);
@@ -236,14 +244,14 @@ __global__ void __launch_bounds__(THREADS) k_fwd(const Args a) {
 }
 
 // dQ by query rows; also D, for the key sweep.
-template <typename T>
-__global__ void __launch_bounds__(THREADS) k_bwd_q(const Args a) {
+template <typename T, int RPT>
+__global__ void __launch_bounds__(THREADS, 2) k_bwd_q(const Args a) {
     extern __shared__ __align__(16) float sh[];
     __shared__ uint32_t words[2];
-    float *Q = sh, *dO = Q + TILE, *K = dO + TILE, *V = K + TILE, *S = V + TILE;
+    float *Q = sh, *dO = Q + rtile(RPT), *S = dO + rtile(RPT), *K = S + rtile(RPT), *V = K + TILE;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
-    RowTile rt;
+    RowTile<RPT> rt;
     rt.init(a, ty);
     const int n = (rt.jhi - rt.jlo + 64) / 64;
     auto qrow = [&](const View& x, int r) -> const T* {
@@ -252,29 +260,29 @@ __global__ void __launch_bounds__(THREADS) k_bwd_q(const Args a) {
         const long long p = rt.first + t;
         return p >= 0 && p < a.Lk && a.live(rt.b, (int)p) ? x.at<T>(rt.b, h, t) : nullptr;
     };
-    load_tile<T>(Q, [&](int r) { return qrow(a.q, r); });
-    load_tile<T>(dO, [&](int r) { return qrow(a.dO, r); });
+    load_tile<T, 16 * RPT>(Q, [&](int r) { return qrow(a.q, r); });
+    load_tile<T, 16 * RPT>(dO, [&](int r) { return qrow(a.dO, r); });
     __syncthreads();
-    float u2[4], D[4];
+    float u2[RPT], D[RPT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RPT; ++i) {
         u2[i] = D[i] = 0.f;
         int h, t;
-        if (!rt.row(a, ty * 4 + i, h, t)) h = -1;
+        if (!rt.row(a, ty * RPT + i, h, t)) h = -1;
         if (h >= 0) u2[i] = a.u[((long long)rt.b * a.Hq + h) * a.Lq + t] * kLog2e;
         if (!a.exact_d) {
             float dot = 0.f;
-            if (const T* o = qrow(a.o, ty * 4 + i)) {
-                const float* g = dO + (ty * 4 + i) * LD + tx * 4;
+            if (const T* o = qrow(a.o, ty * RPT + i)) {
+                const float* g = dO + (ty * RPT + i) * LD + tx * 4;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) dot = fmaf(to_f32(o[tx * 4 + e]), g[e], dot);
             }
             D[i] = sum16(dot);
         }
     }
-    uint64_t acc[4][2];
+    uint64_t acc[RPT][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = 0;
+    for (int i = 0; i < RPT; ++i) acc[i][0] = acc[i][1] = 0;
     // with exact_d the keys are walked twice: first D = sum_j P <dO, V_j>, then dQ
     const int first_pass = a.exact_d ? n : 0;
     for (int x = 0; x < n + first_pass; ++x) {
@@ -286,34 +294,34 @@ __global__ void __launch_bounds__(THREADS) k_bwd_q(const Args a) {
             const int j = c0 + r;
             return j <= rt.jhi && a.live(rt.b, j) ? y.at<T>(rt.b, rt.hk, j) : nullptr;
         };
-        load_tile<T>(K, [&](int r) { return row(a.k, r); });
-        load_tile<T>(V, [&](int r) { return row(a.v, r); });
+        load_tile<T, 64>(K, [&](int r) { return row(a.k, r); });
+        load_tile<T, 64>(V, [&](int r) { return row(a.v, r); });
         __syncthreads();
-        float s[4][4], g[4][4];
-        mm_abt(Q, K, ty, tx, s);
-        mm_abt(dO, V, ty, tx, g);
+        float s[RPT][4], g[RPT][4];
+        mm_abt<RPT>(Q, K, ty, tx, s);
+        mm_abt<RPT>(dO, V, ty, tx, g);
         if (a.exact_d && x == first_pass) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) D[i] = sum16(D[i]);
+            for (int i = 0; i < RPT; ++i) D[i] = sum16(D[i]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RPT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int jj = tx + 16 * j, key = c0 + jj;
                 const bool on = key >= rt.lo[i] && key <= rt.hi[i] && live_bit(words, jj);
                 const float p = on ? ex2(fmaf(s[i][j], a.c2, u2[i])) : 0.f;
                 if (sum) D[i] += on ? p * g[i][j] : 0.f;
-                else S[(ty * 4 + i) * LD + jj] = on ? p * (g[i][j] - D[i]) : 0.f;
+                else S[(ty * RPT + i) * LD + jj] = on ? p * (g[i][j] - D[i]) : 0.f;
             }
         if (sum) continue;
         __syncwarp();
-        mm_ab(S, K, ty, tx, acc);
+        mm_ab<RPT>(S, K, ty, tx, acc);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < RPT; ++i) {
         int h, t;
-        if (!rt.row(a, ty * 4 + i, h, t)) continue;
+        if (!rt.row(a, ty * RPT + i, h, t)) continue;
         float x[4];
         tc::upk2(acc[i][0], x[0], x[1]);
         tc::upk2(acc[i][1], x[2], x[3]);
@@ -323,37 +331,38 @@ __global__ void __launch_bounds__(THREADS) k_bwd_q(const Args a) {
 }
 
 // dK and dV by key rows: the queries of every head of the group whose band holds the keys.
-template <typename T>
-__global__ void __launch_bounds__(THREADS) k_bwd_kv(const Args a) {
+template <typename T, int RPT>
+__global__ void __launch_bounds__(THREADS, 2) k_bwd_kv(const Args a) {
     extern __shared__ __align__(16) float sh[];
     __shared__ uint32_t words[2];
     __shared__ float u2[64], D[64];
-    float *K = sh, *V = K + TILE, *Q = V + TILE, *dO = Q + TILE, *P = dO + TILE, *S = P + TILE;
+    float *K = sh, *V = K + rtile(RPT), *P = V + rtile(RPT), *S = P + rtile(RPT), *Q = S + rtile(RPT), *dO = Q + TILE;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     int x = blockIdx.x;
-    const int j0 = (x % a.ntile) * 64;
+    constexpr int M = 16 * RPT;
+    const int j0 = (x % a.ntile) * M;
     x /= a.ntile;
     const int hk = x % a.Hk, b = x / a.Hk;
     const long long first = a.first(b);
-    // queries whose position lies in [j0 - R, j0 + 63 + W] and in the span
+    // queries whose position lies in [j0 - R, j0 + M - 1 + W] and in the span
     const int2 sp = span(a, b);
     const long long pl = j0 - (long long)a.R > sp.x ? j0 - (long long)a.R : sp.x;
-    const long long ph = (long long)j0 + 63 + a.W < sp.y ? (long long)j0 + 63 + a.W : sp.y;
+    const long long ph = (long long)j0 + M - 1 + a.W < sp.y ? (long long)j0 + M - 1 + a.W : sp.y;
     const long long il = pl - first > 0 ? pl - first : 0;
     const long long ih = ph - first < a.Lq - 1 ? ph - first : a.Lq - 1;
-    const int n = ih < il || j0 > sp.y || j0 + 63 < sp.x ? 0 : (int)((ih - il) / 64 + 1);
+    const int n = ih < il || j0 > sp.y || j0 + M - 1 < sp.x ? 0 : (int)((ih - il) / 64 + 1);
     auto krow = [&](const View& y, int r) -> const T* {
         const int j = j0 + r;
         return j < a.Lk && a.live(b, j) ? y.at<T>(b, hk, j) : nullptr;
     };
-    load_tile<T>(K, [&](int r) { return krow(a.k, r); });
-    load_tile<T>(V, [&](int r) { return krow(a.v, r); });
-    bool ok[4];
+    load_tile<T, 16 * RPT>(K, [&](int r) { return krow(a.k, r); });
+    load_tile<T, 16 * RPT>(V, [&](int r) { return krow(a.v, r); });
+    bool ok[RPT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) ok[i] = krow(a.k, ty * 4 + i) != nullptr;
-    uint64_t dk[4][2], dv[4][2];
+    for (int i = 0; i < RPT; ++i) ok[i] = krow(a.k, ty * RPT + i) != nullptr;
+    uint64_t dk[RPT][2], dv[RPT][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dk[i][0] = dk[i][1] = dv[i][0] = dv[i][1] = 0;
+    for (int i = 0; i < RPT; ++i) dk[i][0] = dk[i][1] = dv[i][0] = dv[i][1] = 0;
     for (int y = 0; y < n * a.G; ++y) {
         const int h = hk * a.G + y / n;
         const int t0 = (int)il + 64 * (y % n);
@@ -371,30 +380,30 @@ __global__ void __launch_bounds__(THREADS) k_bwd_kv(const Args a) {
             const int t = t0 + r;
             return t <= ih && a.live(b, (int)(first + t)) ? z.at<T>(b, h, t) : nullptr;
         };
-        load_tile<T>(Q, [&](int r) { return row(a.q, r); });
-        load_tile<T>(dO, [&](int r) { return row(a.dO, r); });
+        load_tile<T, 64>(Q, [&](int r) { return row(a.q, r); });
+        load_tile<T, 64>(dO, [&](int r) { return row(a.dO, r); });
         __syncthreads();
-        float s[4][4], g[4][4];
-        mm_abt(K, Q, ty, tx, s);
-        mm_abt(V, dO, ty, tx, g);
+        float s[RPT][4], g[RPT][4];
+        mm_abt<RPT>(K, Q, ty, tx, s);
+        mm_abt<RPT>(V, dO, ty, tx, g);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RPT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int jj = tx + 16 * j;
-                const long long gap = first + t0 + jj - (j0 + ty * 4 + i);  // query's position less the key's
+                const long long gap = first + t0 + jj - (j0 + ty * RPT + i);  // query's position less the key's
                 const bool on = ok[i] && live_bit(words, jj) && gap <= a.W && gap >= -(long long)a.R;
                 const float p = on ? ex2(fmaf(s[i][j], a.c2, u2[jj])) : 0.f;
-                P[(ty * 4 + i) * LD + jj] = p;
-                S[(ty * 4 + i) * LD + jj] = on ? p * (g[i][j] - D[jj]) : 0.f;
+                P[(ty * RPT + i) * LD + jj] = p;
+                S[(ty * RPT + i) * LD + jj] = on ? p * (g[i][j] - D[jj]) : 0.f;
             }
         __syncwarp();
-        mm_ab(P, dO, ty, tx, dv);
-        mm_ab(S, Q, ty, tx, dk);
+        mm_ab<RPT>(P, dO, ty, tx, dv);
+        mm_ab<RPT>(S, Q, ty, tx, dk);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int j = j0 + ty * 4 + i;
+    for (int i = 0; i < RPT; ++i) {
+        const int j = j0 + ty * RPT + i;
         if (j >= a.Lk) continue;
         float z[4];
         tc::upk2(dv[i][0], z[0], z[1]);
