@@ -141,7 +141,7 @@ void base_args(sm::Args* a, const sa_softmax_params* p, const Plan& pl, const ui
 template <int RPT>
 cudaError_t fwd_simt(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
     const long long tiles = (long long)p->B * p->Hk * pl.ntile;
-    return launch(sm::simt::k_fwd<float, RPT>, tiles * pl.nsplit, sm::simt::THREADS, sm::simt::smem_bytes(RPT, 2, 2), st,
+    return launch(sm::simt::k_fwd<RPT>, tiles * pl.nsplit, sm::simt::THREADS, sm::simt::smem_bytes(RPT, 2, 2 * sm::simt::nbuf(RPT, false)), st,
                   a);
 }
 
@@ -208,10 +208,10 @@ template <int RPT>
 cudaError_t bwd_simt(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cudaStream_t st) {
     using namespace sm::simt;
     const long long BH = (long long)p->B * p->Hk;
-    const cudaError_t e = launch(k_bwd_q<float, RPT>, BH * a.ntile, THREADS, smem_bytes(RPT, 3, 2), st, a);
+    const cudaError_t e = launch(k_bwd_q<RPT>, BH * a.ntile, THREADS, smem_bytes(RPT, 3, 2 * nbuf(RPT, true)), st, a);
     if (e != cudaSuccess) return e;
     a.ntile = pl.nktile;
-    return launch(k_bwd_kv<float, RPT>, BH * pl.nktile, THREADS, smem_bytes(RPT, 4, 2), st, a);
+    return launch(k_bwd_kv<RPT>, BH * pl.nktile, THREADS, smem_bytes(RPT, 4, 2 * nbuf(RPT, true)), st, a);
 }
 
 template <int MODE, bool EXACT>

@@ -20,6 +20,9 @@ constexpr int TILE = 64 * LD;
 __host__ __device__ constexpr int rtile(int rpt) { return 16 * rpt * LD; }
 // bytes of `r` row tiles and `c` chunk tiles
 __host__ __device__ constexpr int smem_bytes(int rpt, int r, int c) { return (r * rtile(rpt) + c * TILE) * 4; }
+// chunk buffers: two, the next chunk's copies in flight during this one's
+// products, where two blocks still fit an SM
+__host__ __device__ constexpr int nbuf(int rpt, bool bwd) { return bwd && rpt == 4 ? 1 : 2; }
 
 // s[i][j] = sum_k A[ty * RPT + i][k] B[tx + 16 j][k] (even and odd k apart, then together)
 template <int RPT>
@@ -96,6 +99,21 @@ __device__ __forceinline__ void load_tile(float* dst, F base) {
     }
 }
 
+// The same by cp.async, 16 bytes at a time (fp32).
+template <int ROWS, typename F>
+__device__ __forceinline__ void copy_tile(float* dst, const float* any, F base) {
+#pragma unroll
+    for (int x = threadIdx.x; x < ROWS * 16; x += THREADS) {
+        const int r = x >> 4, c = (x & 15) * 4;
+        const float* p = base(r);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst + r * LD + c)),
+                     "l"(p ? p + c : any), "r"(p ? 16 : 0)
+                     : "memory");
+    }
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
 __device__ __forceinline__ float sum16(float x) {
 #pragma unroll
     for (int m = 8; m; m >>= 1) x += __shfl_xor_sync(~0u, x, m);
@@ -156,11 +174,12 @@ __device__ __forceinline__ void live_keys(const Args& a, int b, int c0, uint32_t
 __device__ __forceinline__ bool live_bit(const uint32_t* words, int j) { return (words[j >> 5] >> (j & 31)) & 1u; }
 
 // One pass over the keys with the running maximum and sum of each row.
-template <typename T, int RPT>
+template <int RPT>
 __global__ void __launch_bounds__(THREADS, 2) k_fwd(const Args a) {
+    using T = float;
     extern __shared__ __align__(16) float sh[];
-    __shared__ uint32_t words[2];
-    float *Q = sh, *P = Q + rtile(RPT), *K = P + rtile(RPT), *V = K + TILE;
+    __shared__ uint32_t words[2][2];
+    float *Q = sh, *P = Q + rtile(RPT), *K0 = P + rtile(RPT);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
     RowTile<RPT> rt;
@@ -179,17 +198,25 @@ __global__ void __launch_bounds__(THREADS, 2) k_fwd(const Args a) {
         l[i] = 0.f;
         o[i][0] = o[i][1] = 0;
     }
-    for (int ch = n0; ch < n1; ++ch) {
-        const int c0 = rt.jlo + 64 * ch;
-        __syncthreads();
-        live_keys(a, rt.b, c0, words);
+    constexpr int NB = nbuf(RPT, false);
+    auto fetch = [&](int ch) {
+        const int c0 = rt.jlo + 64 * ch, bf = ch % NB;
         auto row = [&](const View& x, int r) -> const T* {
             const int j = c0 + r;
             return j <= rt.jhi && a.live(rt.b, j) ? x.at<T>(rt.b, rt.hk, j) : nullptr;
         };
-        load_tile<T, 64>(K, [&](int r) { return row(a.k, r); });
-        load_tile<T, 64>(V, [&](int r) { return row(a.v, r); });
+        copy_tile<64>(K0 + 2 * bf * TILE, a.k.at<T>(0, 0, 0), [&](int r) { return row(a.k, r); });
+        copy_tile<64>(K0 + (2 * bf + 1) * TILE, a.v.at<T>(0, 0, 0), [&](int r) { return row(a.v, r); });
+        copy_commit();
+    };
+    if (n0 < n1) fetch(n0);
+    for (int ch = n0; ch < n1; ++ch) {
+        const int c0 = rt.jlo + 64 * ch, bf = ch % NB;
+        const float *K = K0 + 2 * bf * TILE, *V = K + TILE;
+        live_keys(a, rt.b, c0, words[ch & 1]);
+        copy_wait();
         __syncthreads();
+        if (ch + 1 < n1) fetch(ch + 1);
         float s[RPT][4];
         mm_abt<RPT>(Q, K, ty, tx, s);
 #pragma unroll
@@ -198,7 +225,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_fwd(const Args a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int jj = tx + 16 * j, key = c0 + jj;
-                const bool on = key >= rt.lo[i] && key <= rt.hi[i] && live_bit(words, jj);
+                const bool on = key >= rt.lo[i] && key <= rt.hi[i] && live_bit(words[ch & 1], jj);
                 s[i][j] = on ? s[i][j] * a.c2 : -INFINITY;
                 top = fmaxf(top, s[i][j]);
             }
@@ -244,11 +271,12 @@ __global__ void __launch_bounds__(THREADS, 2) k_fwd(const Args a) {
 }
 
 // dQ by query rows; also D, for the key sweep.
-template <typename T, int RPT>
+template <int RPT>
 __global__ void __launch_bounds__(THREADS, 2) k_bwd_q(const Args a) {
+    using T = float;
     extern __shared__ __align__(16) float sh[];
-    __shared__ uint32_t words[2];
-    float *Q = sh, *dO = Q + rtile(RPT), *S = dO + rtile(RPT), *K = S + rtile(RPT), *V = K + TILE;
+    __shared__ uint32_t words[2][2];
+    float *Q = sh, *dO = Q + rtile(RPT), *S = dO + rtile(RPT), *K0 = S + rtile(RPT);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
     RowTile<RPT> rt;
@@ -266,57 +294,57 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_q(const Args a) {
     float u2[RPT], D[RPT];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-        u2[i] = D[i] = 0.f;
+        u2[i] = 0.f;
         int h, t;
         if (!rt.row(a, ty * RPT + i, h, t)) h = -1;
         if (h >= 0) u2[i] = a.u[((long long)rt.b * a.Hq + h) * a.Lq + t] * kLog2e;
-        if (!a.exact_d) {
-            float dot = 0.f;
-            if (const T* o = qrow(a.o, ty * RPT + i)) {
-                const float* g = dO + (ty * RPT + i) * LD + tx * 4;
+        float dot = 0.f;
+        if (const T* o = qrow(a.o, ty * RPT + i)) {
+            const float* g = dO + (ty * RPT + i) * LD + tx * 4;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) dot = fmaf(to_f32(o[tx * 4 + e]), g[e], dot);
-            }
-            D[i] = sum16(dot);
+            for (int e = 0; e < 4; ++e) dot = fmaf(o[tx * 4 + e], g[e], dot);
         }
+        D[i] = sum16(dot);
     }
     uint64_t acc[RPT][2];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) acc[i][0] = acc[i][1] = 0;
-    // with exact_d the keys are walked twice: first D = sum_j P <dO, V_j>, then dQ
-    const int first_pass = a.exact_d ? n : 0;
-    for (int x = 0; x < n + first_pass; ++x) {
-        const bool sum = x < first_pass;
-        const int c0 = rt.jlo + 64 * (sum ? x : x - first_pass);
-        __syncthreads();
-        live_keys(a, rt.b, c0, words);
-        auto row = [&](const View& y, int r) -> const T* {
+    constexpr int NB = nbuf(RPT, true);
+    auto fetch = [&](int ch) {
+        const int c0 = rt.jlo + 64 * ch, bf = ch % NB;
+        auto row = [&](const View& x, int r) -> const T* {
             const int j = c0 + r;
-            return j <= rt.jhi && a.live(rt.b, j) ? y.at<T>(rt.b, rt.hk, j) : nullptr;
+            return j <= rt.jhi && a.live(rt.b, j) ? x.at<T>(rt.b, rt.hk, j) : nullptr;
         };
-        load_tile<T, 64>(K, [&](int r) { return row(a.k, r); });
-        load_tile<T, 64>(V, [&](int r) { return row(a.v, r); });
+        copy_tile<64>(K0 + 2 * bf * TILE, a.k.at<T>(0, 0, 0), [&](int r) { return row(a.k, r); });
+        copy_tile<64>(K0 + (2 * bf + 1) * TILE, a.v.at<T>(0, 0, 0), [&](int r) { return row(a.v, r); });
+        copy_commit();
+    };
+    if (n > 0) fetch(0);
+    for (int ch = 0; ch < n; ++ch) {
+        const int c0 = rt.jlo + 64 * ch, bf = ch % NB;
+        const float *K = K0 + 2 * bf * TILE, *V = K + TILE;
+        live_keys(a, rt.b, c0, words[ch & 1]);
+        copy_wait();
         __syncthreads();
+        if (NB == 2 && ch + 1 < n) fetch(ch + 1);
         float s[RPT][4], g[RPT][4];
         mm_abt<RPT>(Q, K, ty, tx, s);
         mm_abt<RPT>(dO, V, ty, tx, g);
-        if (a.exact_d && x == first_pass) {
-#pragma unroll
-            for (int i = 0; i < RPT; ++i) D[i] = sum16(D[i]);
-        }
 #pragma unroll
         for (int i = 0; i < RPT; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int jj = tx + 16 * j, key = c0 + jj;
-                const bool on = key >= rt.lo[i] && key <= rt.hi[i] && live_bit(words, jj);
-                const float p = on ? ex2(fmaf(s[i][j], a.c2, u2[i])) : 0.f;
-                if (sum) D[i] += on ? p * g[i][j] : 0.f;
-                else S[(ty * RPT + i) * LD + jj] = on ? p * (g[i][j] - D[i]) : 0.f;
+                const bool on = key >= rt.lo[i] && key <= rt.hi[i] && live_bit(words[ch & 1], jj);
+                S[(ty * RPT + i) * LD + jj] = on ? ex2(fmaf(s[i][j], a.c2, u2[i])) * (g[i][j] - D[i]) : 0.f;
             }
-        if (sum) continue;
-        __syncwarp();
+        __syncwarp();  // a warp writes and reads the same rows of S
         mm_ab<RPT>(S, K, ty, tx, acc);
+        if (NB == 1 && ch + 1 < n) {
+            __syncthreads();
+            fetch(ch + 1);
+        }
     }
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
@@ -331,12 +359,13 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_q(const Args a) {
 }
 
 // dK and dV by key rows: the queries of every head of the group whose band holds the keys.
-template <typename T, int RPT>
+template <int RPT>
 __global__ void __launch_bounds__(THREADS, 2) k_bwd_kv(const Args a) {
+    using T = float;
     extern __shared__ __align__(16) float sh[];
-    __shared__ uint32_t words[2];
-    __shared__ float u2[64], D[64];
-    float *K = sh, *V = K + rtile(RPT), *P = V + rtile(RPT), *S = P + rtile(RPT), *Q = S + rtile(RPT), *dO = Q + TILE;
+    __shared__ uint32_t words[2][2];
+    __shared__ float u2[2][64], D[2][64];
+    float *K = sh, *V = K + rtile(RPT), *P = V + rtile(RPT), *S = P + rtile(RPT), *Q0 = S + rtile(RPT);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     int x = blockIdx.x;
     constexpr int M = 16 * RPT;
@@ -363,26 +392,34 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_kv(const Args a) {
     uint64_t dk[RPT][2], dv[RPT][2];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) dk[i][0] = dk[i][1] = dv[i][0] = dv[i][1] = 0;
-    for (int y = 0; y < n * a.G; ++y) {
-        const int h = hk * a.G + y / n;
-        const int t0 = (int)il + 64 * (y % n);
-        __syncthreads();
+    constexpr int NB = nbuf(RPT, true);
+    const int ny = n * a.G;  // chunks of queries, head after head
+    auto fetch = [&](int y) {
+        const int h = hk * a.G + y / n, t0 = (int)il + 64 * (y % n), bf = y % NB;
         if (threadIdx.x < 64) {
             const int t = t0 + threadIdx.x;
             const bool on = t <= ih && a.live(b, (int)(first + t));
             const uint32_t w = __ballot_sync(~0u, on);
-            if ((threadIdx.x & 31) == 0) words[threadIdx.x >> 5] = w;
+            if ((threadIdx.x & 31) == 0) words[bf][threadIdx.x >> 5] = w;
             const long long at = ((long long)b * a.Hq + h) * a.Lq + t;
-            u2[threadIdx.x] = on ? a.u[at] * kLog2e : 0.f;
-            D[threadIdx.x] = on ? a.D[at] : 0.f;
+            u2[bf][threadIdx.x] = on ? a.u[at] * kLog2e : 0.f;
+            D[bf][threadIdx.x] = on ? a.D[at] : 0.f;
         }
         auto row = [&](const View& z, int r) -> const T* {
             const int t = t0 + r;
             return t <= ih && a.live(b, (int)(first + t)) ? z.at<T>(b, h, t) : nullptr;
         };
-        load_tile<T, 64>(Q, [&](int r) { return row(a.q, r); });
-        load_tile<T, 64>(dO, [&](int r) { return row(a.dO, r); });
+        copy_tile<64>(Q0 + 2 * bf * TILE, a.q.at<T>(0, 0, 0), [&](int r) { return row(a.q, r); });
+        copy_tile<64>(Q0 + (2 * bf + 1) * TILE, a.dO.at<T>(0, 0, 0), [&](int r) { return row(a.dO, r); });
+        copy_commit();
+    };
+    if (ny > 0) fetch(0);
+    for (int y = 0; y < ny; ++y) {
+        const int t0 = (int)il + 64 * (y % n), bf = y % NB;
+        const float *Q = Q0 + 2 * bf * TILE, *dO = Q + TILE;
+        copy_wait();
         __syncthreads();
+        if (NB == 2 && y + 1 < ny) fetch(y + 1);
         float s[RPT][4], g[RPT][4];
         mm_abt<RPT>(K, Q, ty, tx, s);
         mm_abt<RPT>(V, dO, ty, tx, g);
@@ -392,14 +429,18 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_kv(const Args a) {
             for (int j = 0; j < 4; ++j) {
                 const int jj = tx + 16 * j;
                 const long long gap = first + t0 + jj - (j0 + ty * RPT + i);  // query's position less the key's
-                const bool on = ok[i] && live_bit(words, jj) && gap <= a.W && gap >= -(long long)a.R;
-                const float p = on ? ex2(fmaf(s[i][j], a.c2, u2[jj])) : 0.f;
+                const bool on = ok[i] && live_bit(words[bf], jj) && gap <= a.W && gap >= -(long long)a.R;
+                const float p = on ? ex2(fmaf(s[i][j], a.c2, u2[bf][jj])) : 0.f;
                 P[(ty * RPT + i) * LD + jj] = p;
-                S[(ty * RPT + i) * LD + jj] = on ? p * (g[i][j] - D[jj]) : 0.f;
+                S[(ty * RPT + i) * LD + jj] = on ? p * (g[i][j] - D[bf][jj]) : 0.f;
             }
         __syncwarp();
         mm_ab<RPT>(P, dO, ty, tx, dv);
         mm_ab<RPT>(S, Q, ty, tx, dk);
+        if (NB == 1 && y + 1 < ny) {
+            __syncthreads();
+            fetch(y + 1);
+        }
     }
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
