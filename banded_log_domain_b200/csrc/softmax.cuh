@@ -29,7 +29,8 @@ struct Args {
     int2* span;           // [B]: first and last unmasked token, with a mask
     View q, k, v, o, dO, dq, dk, dv;
     float* u;             // [B][Hq][Lq]
-    float* D;             // [B][Hq][Lq], backward
+    float* D;             // [B][Hq][Lq], backward, fp32
+    uint4* aug;           // [B][Hq][Lq][2], bf16: u / c and -D as 16 more channels of a query
     int* status;
     int nq;               // queries per tile and head
     int ntile;            // query (dK, dV: key) tiles per sequence and key head

@@ -81,7 +81,7 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     const size_t head = kHeader + align_up((size_t)p->B * 8);
     pl->part_ml = head + align_up((size_t)parts * kD * 4);
     pl->fwd_bytes = pl->part_ml + align_up((size_t)parts * 8);
-    pl->bwd_bytes = head + align_up((size_t)pl->rows * 4);
+    pl->bwd_bytes = head + align_up((size_t)pl->rows * (pl->tc ? 32 : 4));
     return SA_OK;
 }
 
@@ -214,17 +214,33 @@ cudaError_t bwd_simt(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cu
     return launch(k_bwd_kv<RPT>, BH * pl.nktile, THREADS, smem_bytes(RPT, 4, 2 * nbuf(RPT, true)), st, a);
 }
 
+// The queries' further channels, [rows of B Hq][Lq][16] bf16: boxes of 64
+// queries, 32-byte swizzle.
+bool make_map_aug(CUtensorMap* m, void* p, int L, int BH) {
+    auto fn = encode_tiled();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {16, (cuuint64_t)L, (cuuint64_t)BH};
+    cuuint64_t strides[2] = {32, (cuuint64_t)L * 32};
+    cuuint32_t box[3] = {16, 64, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, p, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_32B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int MODE, bool EXACT>
 cudaError_t bwd_tc(const sa_softmax_params* p, const sm::Args& a, long long items, cudaStream_t st) {
     using namespace sm::tcf::bwd;
     Maps maps;
+    std::memset(&maps, 0, sizeof(maps));
     bool ok = true;
     if (MODE == DQ)
         ok = make_map(&maps.R1, a.q, p->B, p->Hq, p->Lq, a.nq, a.G) && make_map(&maps.R2, a.dO, p->B, p->Hq, p->Lq, a.nq, a.G) &&
              make_map(&maps.C1, a.k, p->B, p->Hk, p->Lk, 64, 1) && make_map(&maps.C2, a.v, p->B, p->Hk, p->Lk, 64, 1);
     else
         ok = make_map(&maps.R1, a.k, p->B, p->Hk, p->Lk, 128, 1) && make_map(&maps.R2, a.v, p->B, p->Hk, p->Lk, 128, 1) &&
-             make_map(&maps.C1, a.q, p->B, p->Hq, p->Lq, 64, 1) && make_map(&maps.C2, a.dO, p->B, p->Hq, p->Lq, 64, 1);
+             make_map(&maps.C1, a.q, p->B, p->Hq, p->Lq, 64, 1) && make_map(&maps.C2, a.dO, p->B, p->Hq, p->Lq, 64, 1) &&
+             make_map_aug(&maps.X, a.aug, p->Lq, p->B * p->Hq);
     if (!ok) return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)std::min<long long>(items, sm_count());
     cudaError_t e = cudaFuncSetAttribute(tc_bwd<MODE, EXACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
@@ -319,6 +335,7 @@ sa_status sinkhorn_attn_softmax_bwd(const sa_softmax_params* p, const void* q, c
         return SA_ERR_INVALID_ARG;
     a.u = const_cast<float*>(u);
     a.D = (float*)((char*)ws + kHeader + align_up((size_t)p->B * 8));
+    a.aug = (uint4*)a.D;
     // With few keys a row's probabilities are large and dO . O, taken from the
     // rounded O, is off by about as much as the dS it is subtracted in: up to
     // 64 keys the sweep forms D itself, in a pass of its own over them.

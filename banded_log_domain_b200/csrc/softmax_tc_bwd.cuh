@@ -14,9 +14,12 @@
 // from, from where the second products read them as their A operand.  Two teams
 // take the units in turn.  One warp issues S and G, another the second products
 // (one thread for all that add into an accumulator); a loader brings the tiles,
-// and an aux warp prepares each chunk's columns (mask words; u and D of queries;
-// zeroed operand rows of tokens that are not in use, as 0 times what they hold
-// need not be 0).  D = dO . O is formed by the teams' warps at an item's start, a
+// and an aux warp prepares each chunk's columns (mask words; zeroed operand rows
+// of tokens that are not in use, as 0 times what they hold need not be 0).  In DKV
+// u and D belong to columns: they enter S and G in the products themselves, as 16
+// more channels, u / c and -D in three bf16 parts each (2^-24 of them) against
+// ones; read by every thread from shared memory they cost the teams twice the
+// time, behind the products' own reads.  D = dO . O is formed by the teams' warps at an item's start, a
 // quarter of the channels each; one aux warp for all rows took 20 us an item.
 #pragma once
 
@@ -33,7 +36,7 @@ constexpr int W_LOAD = 16, W_AUX = 17, W_SG = 18, W_AC = 19;
 constexpr int REG_TEAM = 104, REG_OTHER = 64;  // launched with 96 x 640 = 61440
 static_assert(512 * REG_TEAM + 128 * REG_OTHER <= 61440, "register split");
 constexpr int KT = TILE / 2;
-constexpr int NST = 8, NIT = 4, NSLOT = 3;
+constexpr int NST = 7, NIT = 4, NSLOT = 3;
 
 struct Item {
     int b, hk, r0, n, c0, vlo, vhi, pad;  // b < 0: no more; r0: first query or key; c0: column of chunk 0
@@ -43,9 +46,11 @@ struct Item {
 
 constexpr int OFF_R = 0;                        // two buffers of two row tiles
 constexpr int OFF_ST = OFF_R + 4 * TILE;        // stages of two chunk tiles
-constexpr int OFF_ITEM = OFF_ST + NST * 2 * KT;
-constexpr int OFF_COL = OFF_ITEM + NIT * (int)sizeof(Item);  // per stage: u2[64], D[64]
-constexpr int OFF_XD = OFF_COL + NST * 512;     // two buffers of shares of D, [4][128]
+constexpr int AUG = 64 * 32;                    // DKV: a chunk's columns as 16 more channels
+constexpr int OFF_AUG = OFF_ST + NST * 2 * KT;  // one per stage
+constexpr int OFF_ONE = OFF_AUG + NST * AUG;    // and the rows' side, 128 x 32 bytes for S, for G
+constexpr int OFF_ITEM = OFF_ONE + 2 * 4096;
+constexpr int OFF_XD = OFF_ITEM + NIT * (int)sizeof(Item);  // two buffers of shares of D, [4][128]
 constexpr int OFF_WORDS = OFF_XD + 4096;
 constexpr int OFF_BAR = OFF_WORDS + NST * 8;
 enum { RFULL = 0, REMPTY = 2, IFULL = 4, IEMPTY = IFULL + NIT, SGFULL = IEMPTY + NIT, DSFULL = SGFULL + NSLOT, SLOT = DSFULL + NSLOT, ACCFULL = SLOT + NSLOT,
@@ -53,11 +58,25 @@ enum { RFULL = 0, REMPTY = 2, IFULL = 4, IEMPTY = IFULL + NIT, SGFULL = IEMPTY +
        EMPTY = READY + NST, NBAR = EMPTY + NST };
 constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
 static_assert(SMEM <= 227 * 1024, "shared memory");
-static_assert(sizeof(Item) % 8 == 0 && OFF_COL % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
+static_assert(sizeof(Item) % 8 == 0 && OFF_BAR % 8 == 0, "alignment");
 
 struct Maps {
     CUtensorMap R1, R2, C1, C2;  // DQ: Q, dO, K, V;  DKV: K, V, Q, dO
+    CUtensorMap X;               // DKV: the queries' 16 further channels
 };
+
+// Byte offset of 16-byte piece c (0, 1) of row r in a tile of 32-byte rows, 32-byte swizzle.
+__device__ __forceinline__ uint32_t aug_off(int r, int c) { return r * 32 + ((c ^ ((r >> 2) & 1)) << 4); }
+// x as hi + mid + lo in bf16: the two words of slots 0-1 and 2-3 (3: next).
+__device__ __forceinline__ void split3(float x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    const __nv_bfloat16 h = __float2bfloat16_rn(x);
+    const float y = x - __bfloat162float(h);
+    const __nv_bfloat16 m = __float2bfloat16_rn(y);
+    const __nv_bfloat16 l = __float2bfloat16_rn(y - __bfloat162float(m));
+    hi = __bfloat16_as_ushort(h);
+    mid = __bfloat16_as_ushort(m);
+    lo = __bfloat16_as_ushort(l);
+}
 
 template <int MODE>
 __device__ __forceinline__ void make_item(const Args& a, int idx, Item& w) {
@@ -100,7 +119,6 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tbase + 1);
     uint32_t* words = reinterpret_cast<uint32_t*>(sm + OFF_WORDS);
     Item* items = reinterpret_cast<Item*>(sm + OFF_ITEM);
-    float* cols = reinterpret_cast<float*>(sm + OFF_COL);
     float* xd = reinterpret_cast<float*>(sm + OFF_XD);
     Ctl ctl{bar, abort_flag, a.status};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -131,6 +149,15 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
         tc::mbar_init(bar + DRAIN, 2);
         *abort_flag = 0;
         tc::fence_mbar_init();
+    }
+    if (MODE == DKV) {  // the constant rows: 1 in slots 0-2 (S) or 3-5 (G) of 16
+        for (int x = threadIdx.x; x < 512; x += THREADS) {
+            const int r = x & 127, c = (x >> 7) & 1, t = x >> 8;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (c == 0) w = t == 0 ? make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u) : make_uint4(0u, 0x3f800000u, 0x3f803f80u, 0u);
+            *reinterpret_cast<uint4*>(sm + OFF_ONE + t * 4096 + aug_off(r, c)) = w;
+        }
+        tc::fence_async_smem();
     }
     if (warp == 0) {
         tc::tmem_alloc(tbase, 512);
@@ -189,7 +216,9 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                                 break;
                             }
                             uint8_t* st = sm + OFF_ST + s * 2 * KT;
-                            tc::mbar_expect_tx(bar + FULL + s, 2 * KT);
+                            tc::mbar_expect_tx(bar + FULL + s, 2 * KT + (MODE == DKV ? AUG : 0));
+                            if (MODE == DKV)
+                                tc::tma_load_3d(sm + OFF_AUG + s * AUG, &maps.X, bar + FULL + s, 0, c0 + 64 * c, b * a.Hq + h);
                             tma_load_4d(st, &maps.C1, bar + FULL + s, c0 + 64 * c, h, b);
                             tma_load_4d(st + KT, &maps.C2, bar + FULL + s, c0 + 64 * c, h, b);
                         }
@@ -209,26 +238,17 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             for (int it = 0; ok && begin_item(it); ++it) {
                 const Item& w = items[it % NIT];
                 const int n = w.n, last = w.vhi - w.c0;  // columns 0 .. last, from c0 on
-                // mask of column 0, u and D of the group's first head at column 0
+                // mask of column 0
                 const uint8_t* pm = a.mask ? a.mask + (long long)w.b * a.Lk + w.c0 + (MODE == DKV ? w.first : 0) : nullptr;
-                const long long at = MODE == DKV ? ((long long)w.b * a.Hq + w.hk * a.G) * a.Lq + w.c0 : 0;
-                // the columns of a chunk: this lane's two
                 uint32_t bits[2];
-                float cu[2], cD[2];
-                auto fetch = [&](int p, int c) {
+                auto fetch = [&](int c) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int j = 64 * c + 32 * k + lane;
-                        const bool on = j <= last && (pm == nullptr || pm[j] != 0);
-                        if (MODE == DKV) {
-                            const long long x = at + (long long)p * a.Lq + j;
-                            cu[k] = on ? a.u[x] * kLog2e : 0.f;
-                            cD[k] = on ? a.D[x] : 0.f;
-                        }
-                        bits[k] = __ballot_sync(~0u, on);
+                        bits[k] = __ballot_sync(~0u, j <= last && (pm == nullptr || pm[j] != 0));
                     }
                 };
-                if (n > 0) fetch(0, 0);
+                if (n > 0) fetch(0);
                 for (int p = 0; ok && p < passes; ++p) {
                     for (int c = 0; c < n; ++c, ++gu) {
                         const int s = gu % NST;
@@ -237,14 +257,6 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                             break;
                         }
                         if (lane < 2) words[2 * s + lane] = lane ? bits[1] : bits[0];
-                        if (MODE == DKV) {
-                            float* cv = cols + s * 128;
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                cv[32 * k + lane] = cu[k];
-                                cv[64 + 32 * k + lane] = cD[k];
-                            }
-                        }
                         if ((bits[0] & bits[1]) != ~0u) {
                             uint8_t* x = sm + OFF_ST + s * 2 * KT;
 #pragma unroll
@@ -261,8 +273,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                         }
                         __syncwarp();
                         if (lane == 0) tc::mbar_arrive(bar + READY + s);
-                        if (c + 1 < n) fetch(p, c + 1);
-                        else if (p + 1 < passes) fetch(p + 1, 0);
+                        fetch(c + 1 < n ? c + 1 : 0);
                     }
                 }
                 end_item(it);
@@ -272,6 +283,8 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             const uint32_t id = tc::idesc_bf16(128, 64, false, false);
             const uint64_t dR = tc::sdesc_sw128(tc::smem_u32(sm + OFF_R), 16, 1024);
             const uint64_t dC = tc::sdesc_sw128(tc::smem_u32(sm + OFF_ST), 16, 1024);
+            const uint64_t dOne = tc::sdesc_sw32(tc::smem_u32(sm + OFF_ONE));
+            const uint64_t dAug = tc::sdesc_sw32(tc::smem_u32(sm + OFF_AUG));
             int gu = 0;
             bool ok = true;
             for (int it = 0; ok && begin_item(it); ++it) {
@@ -295,6 +308,10 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                         for (int k = 0; k < 4; ++k)
                             tc::mma_bf16(tm + 128 * x + 64, tc::sdesc_add(dA, TILE + 32 * k),
                                          tc::sdesc_add(dB, KT + 32 * k), id, k > 0);
+                        if (MODE == DKV) {  // S + u / c, G - D
+                            tc::mma_bf16(tm + 128 * x, dOne, tc::sdesc_add(dAug, s * AUG), id, 1u);
+                            tc::mma_bf16(tm + 128 * x + 64, tc::sdesc_add(dOne, 4096), tc::sdesc_add(dAug, s * AUG), id, 1u);
+                        }
                         tc::tc_commit(bar + SGFULL + x);
                     }
                     __syncwarp();
@@ -368,6 +385,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
         const int g = MODE == DQ ? r / a.nq : 0, iq = MODE == DQ ? r % a.nq : r;
         const uint32_t lanebase = (uint32_t)(qd * 32) << 16;
         const uint64_t c2p = tc::pk2(a.c2, a.c2);
+        const float uscale = 1.f / a.c;
         int gu = 0, na = 0, nx = 0;
         bool ok = true;
         // The sum over the four warps that hold a row's columns.  Two buffers: to
@@ -386,7 +404,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             const Item& w = items[it % NIT];
             const int rb = it & 1, n = w.n, nu = n * passes;
             // this row: its columns in the band, relative to chunk 0
-            float u2 = 0.f, D = 0.f;
+            float ur = 0.f, D = 0.f;  // u in units of <q, k>, as the scores
             int lo = 0, hi = -1;
             const int i = w.r0 + iq;  // query or key
             const bool exists = MODE == DQ ? g < a.G && i < a.Lq : i < a.Lk;
@@ -401,7 +419,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                         a.keys(p, lo, hi);
                         lo -= w.c0;
                         hi -= w.c0;
-                        u2 = a.u[at] * kLog2e;
+                        ur = a.u[at] * uscale;
                         if (!EXACT) {
                             const uint4* po = reinterpret_cast<const uint4*>(
                                 a.o.at<__nv_bfloat16>(w.b, w.hk * a.G + g, i) + 16 * q4);
@@ -454,7 +472,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                 if (u >= nu) break;
                 while (c >= n) c -= n;
                 const int gv0 = gu + u, s = gv0 % NST, x = gv0 % NSLOT;
-                if (((MODE == DKV || a.mask) && !ctl.wait_warp(READY + s, (gv0 / NST) & 1)) ||
+                if ((a.mask && !ctl.wait_warp(READY + s, (gv0 / NST) & 1)) ||
                     !ctl.wait_warp(SGFULL + x, (gv0 / NSLOT) & 1)) {
                     ok = false;
                     break;
@@ -475,7 +493,6 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                         for (int j = 0; j < 16; ++j) pw[j] = 0u;
                     }
                 } else {
-                    const float* cv = cols + s * 128 + 32 * hf;
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {  // 16 columns at a time
                         uint32_t sv[16], gv[16];
@@ -493,31 +510,23 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                                 }
                         }
 #pragma unroll
-                        for (int j = 0; j < 8; j += 2) {
-                            ulonglong2 up, dp;
-                            if (MODE == DKV) {
-                                up = *reinterpret_cast<const ulonglong2*>(cv + 16 * z + 2 * j);
-                                dp = *reinterpret_cast<const ulonglong2*>(cv + 64 + 16 * z + 2 * j);
+                        for (int j = 0; j < 8; ++j) {
+                            uint64_t x2 = tc::pk2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1]));
+                            uint64_t d2 = tc::pk2(__uint_as_float(gv[2 * j]), __uint_as_float(gv[2 * j + 1]));
+                            if (MODE == DQ) {  // in DKV the products have u and D in them
+                                x2 = mul2(tc::add2(x2, tc::pk2(ur, ur)), c2p);
+                                d2 = tc::sub2(d2, tc::pk2(D, D));
                             } else {
-                                up.x = up.y = tc::pk2(u2, u2);
-                                dp.x = dp.y = tc::pk2(D, D);
+                                x2 = mul2(x2, c2p);
                             }
-#pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const int k = 2 * (j + y);
-                                const uint64_t xx = tc::fma2(
-                                    tc::pk2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), c2p, y ? up.y : up.x);
-                                const uint64_t d = tc::sub2(tc::pk2(__uint_as_float(gv[k]), __uint_as_float(gv[k + 1])),
-                                                            y ? dp.y : dp.x);
-                                float e0, e1, d0, d1;
-                                tc::upk2(xx, e0, e1);
-                                e0 = ex2(e0);
-                                e1 = ex2(e1);
-                                tc::upk2(mul2(d, tc::pk2(e0, e1)), d0, d1);
-                                if (EXACT && only_sum) sum += d0 + d1;
-                                dw[8 * z + j + y] = tc::pack_bf16(d0, d1);
-                                if constexpr (MODE == DKV) pw[8 * z + j + y] = tc::pack_bf16(e0, e1);
-                            }
+                            float e0, e1, d0, d1;
+                            tc::upk2(x2, e0, e1);
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                            tc::upk2(mul2(d2, tc::pk2(e0, e1)), d0, d1);
+                            if (EXACT && only_sum) sum += d0 + d1;
+                            dw[8 * z + j] = tc::pack_bf16(d0, d1);
+                            if constexpr (MODE == DKV) pw[8 * z + j] = tc::pack_bf16(e0, e1);
                         }
                     }
                 }
@@ -575,7 +584,13 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bar + ACCEMPTY + ab);
             }
-            if (MODE == DQ && exists && q4 == 0) a.D[at] = D;
+            if (MODE == DQ && exists && q4 == 0) {  // for the key sweep: u / c and -D
+                uint32_t u0, u1, u2, d0, d1, d2;
+                split3(ur, u0, u1, u2);
+                split3(-D, d0, d1, d2);
+                a.aug[2 * at] = make_uint4(u0 | u1 << 16, u2 | d0 << 16, d1 | d2 << 16, 0u);
+                a.aug[2 * at + 1] = make_uint4(0u, 0u, 0u, 0u);
+            }
             end_item(it);
         }
     }

@@ -408,7 +408,8 @@ typedef struct {
 
 /* Workspace bytes of the two calls below (either pointer may be NULL).  The
  * forward's holds partial rows where few queries have their keys split over
- * several blocks (at most 37 MB); the backward's one float32 per query row. */
+ * several blocks (at most 37 MB); the backward's 4 (fp32) or 32 (bf16) bytes per
+ * query row; both 8 bytes per sequence. */
 sa_status sinkhorn_attn_softmax_workspace_size(const sa_softmax_params* p, size_t* fwd_bytes,
                                                size_t* bwd_bytes);
 

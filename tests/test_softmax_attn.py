@@ -38,7 +38,8 @@ def test_null_params_small_workspace_and_host_pointers():
     assert lib.sinkhorn_attn_softmax_bwd(None, *[None] * 12, 1 << 40, None) == -1
     p = P()
     f, b = sa.sinkhorn_attn_softmax_workspace_size(p)
-    assert b == 512 + (2 * 4 * 50 * 4 + 255) // 256 * 256  # status, spans, D
+    assert b == 512 + 2 * 4 * 50 * 32  # status, spans, 32 bytes per query row
+    assert sa.sinkhorn_attn_softmax_workspace_size(P(dtype=sa.SA_F32))[1] == 512 + (2 * 4 * 50 * 4 + 255) // 256 * 256
     assert lib.sinkhorn_attn_softmax_fwd(ctypes.byref(p), *[None] * 8, f - 1, None) == -3
     assert lib.sinkhorn_attn_softmax_bwd(ctypes.byref(p), *[None] * 12, b - 1, None) == -3
     assert lib.sinkhorn_attn_softmax_fwd(ctypes.byref(p), *[None] * 8, f, None) == -1
@@ -77,7 +78,7 @@ def test_workspace_is_bounded_and_grows_with_the_rows_only():
             f, _ = sa.sinkhorn_attn_softmax_workspace_size(P(B=B, Hq=64, Hk=1, Lq=1, Lk=Lk, W=Lk))
             assert f <= 37 << 20
     f, b = sa.sinkhorn_attn_softmax_workspace_size(P(B=1, Hq=16, Hk=16, Lq=32768, Lk=32768, W=256))
-    assert f == 512 and b == 512 + 16 * 32768 * 4
+    assert f == 512 and b == 512 + 16 * 32768 * 32
 
 
 @pytest.mark.parametrize("kw,status", [
