@@ -7,6 +7,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace sa {
 namespace sm {
@@ -77,6 +78,8 @@ __device__ __forceinline__ void tile_keys(const Args& a, int b, int i0, int i1, 
 // The spans, one block per sequence: padding at either end then costs no tiles.
 __global__ void __launch_bounds__(1024) k_span(const Args a) {
     __shared__ int lo[32], hi[32];
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
     const uint8_t* m = a.mask + (long long)blockIdx.x * a.Lk;
     int x = 0x7fffffff, y = -1;
 #pragma unroll 8
@@ -106,6 +109,7 @@ __global__ void __launch_bounds__(128) k_join(const Args a) {
     const long long rows = (long long)a.B * a.Hq * a.Lq;
     const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
+    tc::grid_dep_wait();
     if (row >= rows) return;
     const float2* ml = a.part_ml + row * a.nparts;
     float m = -INFINITY, l = 0.f;
@@ -137,6 +141,7 @@ __global__ void __launch_bounds__(128) k_join(const Args a) {
 template <typename T>
 __global__ void __launch_bounds__(128) k_zero(const Args a) {
     const long long key = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    tc::grid_dep_wait();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
     if (key >= (long long)a.B * a.Hk * a.Lk) return;
     const int j = (int)(key % a.Lk), lane = threadIdx.x & 31;

@@ -105,14 +105,15 @@ bool view(sm::View* v, const void* ptr, const long long s[3], int B, int H, int 
 
 bool ints_ok(const int* x) { return !x || (((uintptr_t)x & 3u) == 0 && on_current_device(x)); }
 
+// Every kernel here is launched with programmatic stream serialisation and waits
+// (griddepcontrol.wait) before any global access.
 template <typename K>
 cudaError_t launch(K kern, long long grid, int threads, int smem, cudaStream_t st, const sm::Args& a) {
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    kern<<<(unsigned)grid, threads, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(kern, dim3((unsigned)grid), dim3(threads), smem, st, a);
 }
 
 void base_args(sm::Args* a, const sa_softmax_params* p, const Plan& pl, const uint8_t* mask, const int* q_pos,

@@ -79,27 +79,8 @@ __device__ __forceinline__ void mm_ab(const float* P, const float* X, int ty, in
     }
 }
 
-// A tile of ROWS rows base(r) (nullptr: zeros) into shared memory.
-template <typename T, int ROWS, typename F>
-__device__ __forceinline__ void load_tile(float* dst, F base) {
-    constexpr int V = 16 / sizeof(T), PER = 64 / V;
-#pragma unroll
-    for (int x = threadIdx.x; x < ROWS * PER; x += THREADS) {
-        const int r = x / PER, c = (x % PER) * V;
-        const T* p = base(r);
-        float e[V];
-        if (p) load_vec(p + c, e, V);
-        else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) e[i] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < V; i += 4)
-            *reinterpret_cast<float4*>(dst + r * LD + c + i) = make_float4(e[i], e[i + 1], e[i + 2], e[i + 3]);
-    }
-}
-
-// The same by cp.async, 16 bytes at a time (fp32).
+// A tile of ROWS rows base(r) (nullptr: zeros) into shared memory by cp.async, 16
+// bytes at a time.
 template <int ROWS, typename F>
 __device__ __forceinline__ void copy_tile(float* dst, const float* any, F base) {
 #pragma unroll
@@ -181,12 +162,14 @@ __global__ void __launch_bounds__(THREADS, 2) k_fwd(const Args a) {
     __shared__ uint32_t words[2][2];
     float *Q = sh, *P = Q + rtile(RPT), *K0 = P + rtile(RPT);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
     RowTile<RPT> rt;
     rt.init(a, ty);
     const int n = (rt.jhi - rt.jlo + 64) / 64;  // 0 when empty
     const int n0 = (int)((long long)n * rt.part / a.nsplit), n1 = (int)((long long)n * (rt.part + 1) / a.nsplit);
-    load_tile<T, 16 * RPT>(Q, [&](int r) -> const T* {
+    copy_tile<16 * RPT>(Q, a.q.at<T>(0, 0, 0), [&](int r) -> const T* {
         int h, t;
         return rt.row(a, r, h, t) ? a.q.at<T>(rt.b, h, t) : nullptr;
     });
@@ -278,6 +261,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_q(const Args a) {
     __shared__ uint32_t words[2][2];
     float *Q = sh, *dO = Q + rtile(RPT), *S = dO + rtile(RPT), *K0 = S + rtile(RPT);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
     RowTile<RPT> rt;
     rt.init(a, ty);
@@ -288,24 +273,6 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_q(const Args a) {
         const long long p = rt.first + t;
         return p >= 0 && p < a.Lk && a.live(rt.b, (int)p) ? x.at<T>(rt.b, h, t) : nullptr;
     };
-    load_tile<T, 16 * RPT>(Q, [&](int r) { return qrow(a.q, r); });
-    load_tile<T, 16 * RPT>(dO, [&](int r) { return qrow(a.dO, r); });
-    __syncthreads();
-    float u2[RPT], D[RPT];
-#pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-        u2[i] = 0.f;
-        int h, t;
-        if (!rt.row(a, ty * RPT + i, h, t)) h = -1;
-        if (h >= 0) u2[i] = a.u[((long long)rt.b * a.Hq + h) * a.Lq + t] * kLog2e;
-        float dot = 0.f;
-        if (const T* o = qrow(a.o, ty * RPT + i)) {
-            const float* g = dO + (ty * RPT + i) * LD + tx * 4;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dot = fmaf(o[tx * 4 + e], g[e], dot);
-        }
-        D[i] = sum16(dot);
-    }
     uint64_t acc[RPT][2];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) acc[i][0] = acc[i][1] = 0;
@@ -320,7 +287,27 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_q(const Args a) {
         copy_tile<64>(K0 + (2 * bf + 1) * TILE, a.v.at<T>(0, 0, 0), [&](int r) { return row(a.v, r); });
         copy_commit();
     };
+    copy_tile<16 * RPT>(Q, a.q.at<T>(0, 0, 0), [&](int r) { return qrow(a.q, r); });
+    copy_tile<16 * RPT>(dO, a.q.at<T>(0, 0, 0), [&](int r) { return qrow(a.dO, r); });
     if (n > 0) fetch(0);
+    else copy_commit();
+    float u2[RPT], D[RPT];
+    float4 o[RPT];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+        u2[i] = 0.f;
+        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        int h, t;
+        if (rt.row(a, ty * RPT + i, h, t)) u2[i] = a.u[((long long)rt.b * a.Hq + h) * a.Lq + t] * kLog2e;
+        if (const T* x = qrow(a.o, ty * RPT + i)) o[i] = *reinterpret_cast<const float4*>(x + tx * 4);
+    }
+    copy_wait();
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {  // D = dO . O
+        const float4 g = *reinterpret_cast<const float4*>(dO + (ty * RPT + i) * LD + tx * 4);
+        D[i] = sum16(fmaf(o[i].x, g.x, fmaf(o[i].y, g.y, fmaf(o[i].z, g.z, o[i].w * g.w))));
+    }
     for (int ch = 0; ch < n; ++ch) {
         const int c0 = rt.jlo + 64 * ch, bf = ch % NB;
         const float *K = K0 + 2 * bf * TILE, *V = K + TILE;
@@ -367,6 +354,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_kv(const Args a) {
     __shared__ float u2[2][64], D[2][64];
     float *K = sh, *V = K + rtile(RPT), *P = V + rtile(RPT), *S = P + rtile(RPT), *Q0 = S + rtile(RPT);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
     int x = blockIdx.x;
     constexpr int M = 16 * RPT;
     const int j0 = (x % a.ntile) * M;
@@ -384,8 +373,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_kv(const Args a) {
         const int j = j0 + r;
         return j < a.Lk && a.live(b, j) ? y.at<T>(b, hk, j) : nullptr;
     };
-    load_tile<T, 16 * RPT>(K, [&](int r) { return krow(a.k, r); });
-    load_tile<T, 16 * RPT>(V, [&](int r) { return krow(a.v, r); });
+    copy_tile<16 * RPT>(K, a.k.at<T>(0, 0, 0), [&](int r) { return krow(a.k, r); });
+    copy_tile<16 * RPT>(V, a.k.at<T>(0, 0, 0), [&](int r) { return krow(a.v, r); });
     bool ok[RPT];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) ok[i] = krow(a.k, ty * RPT + i) != nullptr;
