@@ -50,8 +50,12 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     pl->nq = (pl->tc ? 128 : 16 * pl->rpt) / pl->G;
     const long long RT = (p->Lq + pl->nq - 1) / pl->nq;  // row tiles
     // The tensor-core forward's items are 4, 2 or 1 row tiles (see softmax_tc.cuh).
+    // One leaves the fewest SMs idle where all tiles fit them at once; of many, two
+    // share the key chunks (long32k: 187 us, four 191, one 237), and four pay once
+    // a tile's band is long (8192 dense tokens: 430 us, two 454).
+    const long long W = std::min(p->W, p->Lk);
     pl->nr = 1;
-    if (pl->tc && RT > 1) pl->nr = BH * ((RT + 3) / 4) >= 4LL * sms ? 4 : 2;
+    if (pl->tc && BH * RT > sms) pl->nr = W >= 4096 && BH * RT >= 6LL * sms ? 4 : 2;
     pl->per = pl->nr * pl->nq;
     pl->ntile = (int)((RT + pl->nr - 1) / pl->nr);
     pl->nktile = (p->Lk + 16 * pl->rpt - 1) / (16 * pl->rpt);
@@ -60,7 +64,6 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     // A few query rows over many keys (single new tokens) would leave most SMs
     // idle: then every tile's keys are cut into parts for about two blocks an
     // SM, of at least four chunks each, joined by a second kernel.
-    const long long W = std::min(p->W, p->Lk);
     const long long keys = std::min<long long>(p->Lk, W + (p->causal ? 0 : W) + pl->per);
     const long long chunks = (keys + 63) / 64;
     pl->nsplit = 1;
