@@ -33,59 +33,62 @@ struct alignas(sizeof(T) * N) Piece {
 };
 
 // NP pairs per thread; HALF: the pair's channels are two pieces of NP elements,
-// else one piece of 2 NP.
+// else one piece of 2 NP.  The heads are taken U at a time, all their loads first;
+// the sines are formed while the first ones are on their way.
 template <typename T, int NP, bool HALF>
 __global__ void __launch_bounds__(256) k_rotary(const RotArgs a) {
     constexpr int NV = HALF ? NP : 2 * NP;  // elements of a piece
+    constexpr int U = sizeof(T) == 4 ? 4 : 1;  // bf16 has twice the pairs, and sines, in a thread
     const int t = blockIdx.x * blockDim.y + threadIdx.y, unit = threadIdx.x, b = blockIdx.z;
     if (t >= a.L) return;
     const int h0 = blockIdx.y * a.hc, h1 = min(a.H, h0 + a.hc);
     const bool turn = unit < a.nrot;
     // first channel of the piece (of its x_a in the half layout)
     const int ch = turn ? unit * NV : a.rot + (unit - a.nrot) * NV;
+    const int half = turn && HALF ? a.rot / 2 : 0;  // x_b's distance
     float cs[NP], sn[NP];
-    if (turn) {
-        const double p = a.pos ? (double)a.pos[(long long)b * a.L + t] : (double)t;
+    for (int h = h0; h < h1; h += U) {
+        Piece<T, NV> x[U], y[HALF ? U : 1];
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            const double turns = p * a.freqs[unit * NP + i] * 0.15915494309189533577;  // 1 / (2 pi)
-            float s, c;
-            sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
-            cs[i] = c * a.scale;
-            sn[i] = (a.inverse ? -s : s) * a.scale;
+        for (int u = 0; u < U; ++u) {
+            if (h + u >= h1) break;
+            const bool isq = h + u < a.Hq;
+            const int hh = isq ? h + u : h + u - a.Hq;
+            const long long* is = isq ? a.qs : a.ks;
+            const T* in = (const T*)(isq ? a.q : a.k) + b * is[0] + hh * is[1] + t * is[2] + ch;
+            x[u] = *reinterpret_cast<const Piece<T, NV>*>(in);
+            if (HALF) y[HALF ? u : 0] = *reinterpret_cast<const Piece<T, NV>*>(in + half);
         }
-    }
-#pragma unroll 2
-    for (int h = h0; h < h1; ++h) {
-        const bool isq = h < a.Hq;
-        const int hh = isq ? h : h - a.Hq;
-        const long long* is = isq ? a.qs : a.ks;
-        const long long* os = isq ? a.qos : a.kos;
-        const T* in = (const T*)(isq ? a.q : a.k) + b * is[0] + hh * is[1] + t * is[2] + ch;
-        T* out = (T*)(isq ? a.qo : a.ko) + b * os[0] + hh * os[1] + t * os[2] + ch;
-        Piece<T, NV> x = *reinterpret_cast<const Piece<T, NV>*>(in);
-        if (!turn) {
-            *reinterpret_cast<Piece<T, NV>*>(out) = x;
-            continue;
-        }
-        if (HALF) {
-            Piece<T, NV> y = *reinterpret_cast<const Piece<T, NV>*>(in + a.rot / 2);
+        if (h == h0 && turn) {
+            const double p = a.pos ? (double)a.pos[(long long)b * a.L + t] : (double)t;
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                const float xa = to_f32(x.x[i % NV]), xb = to_f32(y.x[i % NV]);
-                store_elem(&x.x[i % NV], xa * cs[i] - xb * sn[i]);
-                store_elem(&y.x[i % NV], xa * sn[i] + xb * cs[i]);
+                const double turns = p * a.freqs[unit * NP + i] * 0.15915494309189533577;  // 1 / (2 pi)
+                float s, c;
+                sincospif((float)(2.0 * (turns - rint(turns))), &s, &c);
+                cs[i] = c * a.scale;
+                sn[i] = (a.inverse ? -s : s) * a.scale;
             }
-            *reinterpret_cast<Piece<T, NV>*>(out) = x;
-            *reinterpret_cast<Piece<T, NV>*>(out + a.rot / 2) = y;
-        } else {
+        }
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                const float xa = to_f32(x.x[2 * i % NV]), xb = to_f32(x.x[(2 * i + 1) % NV]);
-                store_elem(&x.x[2 * i % NV], xa * cs[i] - xb * sn[i]);
-                store_elem(&x.x[(2 * i + 1) % NV], xa * sn[i] + xb * cs[i]);
+        for (int u = 0; u < U; ++u) {
+            if (h + u >= h1) break;
+            if (turn) {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    T* pa = HALF ? &x[u].x[i % NV] : &x[u].x[2 * i % NV];
+                    T* pb = HALF ? &y[HALF ? u : 0].x[i % NV] : &x[u].x[(2 * i + 1) % NV];
+                    const float xa = to_f32(*pa), xb = to_f32(*pb);
+                    store_elem(pa, xa * cs[i] - xb * sn[i]);
+                    store_elem(pb, xa * sn[i] + xb * cs[i]);
+                }
             }
-            *reinterpret_cast<Piece<T, NV>*>(out) = x;
+            const bool isq = h + u < a.Hq;
+            const int hh = isq ? h + u : h + u - a.Hq;
+            const long long* os = isq ? a.qos : a.kos;
+            T* out = (T*)(isq ? a.qo : a.ko) + b * os[0] + hh * os[1] + t * os[2] + ch;
+            *reinterpret_cast<Piece<T, NV>*>(out) = x[u];
+            if (HALF && turn) *reinterpret_cast<Piece<T, NV>*>(out + half) = y[HALF ? u : 0];
         }
     }
 }
