@@ -45,8 +45,10 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     pl->tc = p->dtype == SA_BF16;
     const int sms = sm_count();
     const long long BH = (long long)p->B * p->Hk;
-    // fp32 tiles of 64 rows, or of 16 where those would leave SMs without one
-    pl->rpt = pl->G <= 16 && BH * ((p->Lq + 64 / pl->G - 1) / (64 / pl->G)) < sms ? 1 : 4;
+    // fp32 tiles of 64 rows; of 32 or 16, which read more shared memory per
+    // product, where even those find an SM each
+    const long long t64 = BH * ((p->Lq + 64 / pl->G - 1) / (64 / pl->G));
+    pl->rpt = pl->G <= 16 && 4 * t64 <= sms ? 1 : pl->G <= 32 && 2 * t64 <= sms ? 2 : 4;
     pl->nq = (pl->tc ? 128 : 16 * pl->rpt) / pl->G;
     const long long RT = (p->Lq + pl->nq - 1) / pl->nq;  // row tiles
     // The tensor-core forward's items are 4, 2 or 1 row tiles (see softmax_tc.cuh).
@@ -200,7 +202,9 @@ cudaError_t fwd_token(const sa_softmax_params* p, const Plan& pl, const sm::Args
 
 cudaError_t fwd_launch(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
     if (pl.token) return fwd_token(p, pl, a, st);
-    const cudaError_t e = !pl.tc         ? (pl.rpt == 4 ? fwd_simt<4>(p, pl, a, st) : fwd_simt<1>(p, pl, a, st))
+    const cudaError_t e = !pl.tc         ? (pl.rpt == 4   ? fwd_simt<4>(p, pl, a, st)
+                                          : pl.rpt == 2 ? fwd_simt<2>(p, pl, a, st)
+                                                        : fwd_simt<1>(p, pl, a, st))
                           : pl.nr == 4 ? fwd_tc<4>(p, pl, a, st)
                           : pl.nr == 2 ? fwd_tc<2>(p, pl, a, st)
                                        : fwd_tc<1>(p, pl, a, st);
@@ -260,7 +264,10 @@ cudaError_t zero_grads(const sa_softmax_params* p, sm::Args& a, cudaStream_t st)
 }
 
 cudaError_t bwd_launch(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cudaStream_t st) {
-    if (!pl.tc) return pl.rpt == 4 ? bwd_simt<4>(p, pl, a, st) : bwd_simt<1>(p, pl, a, st);
+    if (!pl.tc)
+        return pl.rpt == 4   ? bwd_simt<4>(p, pl, a, st)
+               : pl.rpt == 2 ? bwd_simt<2>(p, pl, a, st)
+                             : bwd_simt<1>(p, pl, a, st);
     const long long BH = (long long)p->B * p->Hk;
     a.nq = pl.nq;
     a.ntile = (p->Lq + a.nq - 1) / a.nq;

@@ -1,8 +1,8 @@
 // Softmax attention on the FP32 pipe (fp32 storage): tiles of 16 RPT rows x 64
 // columns, 256 threads of RPT x 4 entries.  All products are packed f32x2 FMAs on
 // operands in shared memory; bound by FFMA issue and the shared-memory reads that
-// feed it.  RPT is 4; 1 where tiles of 64 rows would leave SMs without one (the
-// 512-token problem's three kernels: 100 -> 40 us).
+// feed it.  RPT is 4; 2 or 1 where the tiles are few (the 512-token problem's
+// three kernels: 98 us with 4, 50 with 1).
 #pragma once
 
 #include "softmax.cuh"
