@@ -24,7 +24,8 @@ struct Plan {
     int G, nq, rpt, nr, per, ntile, nktile, nsplit, nparts;
     int token;  // blocks of the single-token forward, 0 where it does not apply
     long long rows;  // B * Hq * Lq
-    size_t fwd_bytes, bwd_bytes, part_ml, span;  // span: in either workspace
+    int qsplit, ksplit;  // parts of the fp32 backward's tiles
+    size_t fwd_bytes, bwd_bytes, bwd_part, part_ml, span;  // span: in either workspace
 };
 
 sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
@@ -45,17 +46,19 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     pl->tc = p->dtype == SA_BF16;
     const int sms = sm_count();
     const long long BH = (long long)p->B * p->Hk;
+    const long long W = std::min(p->W, p->Lk), span = W + (p->causal ? 0 : W);
     // fp32 tiles of 64 rows; of 32 or 16, which read more shared memory per
-    // product, where even those find an SM each
+    // product, where even those find an SM each and a row's keys are too few to
+    // be cut into parts instead
     const long long t64 = BH * ((p->Lq + 64 / pl->G - 1) / (64 / pl->G));
-    pl->rpt = pl->G <= 16 && 4 * t64 <= sms ? 1 : pl->G <= 32 && 2 * t64 <= sms ? 2 : 4;
+    const bool few = span <= 384;
+    pl->rpt = few && pl->G <= 16 && 4 * t64 <= sms ? 1 : few && pl->G <= 32 && 2 * t64 <= sms ? 2 : 4;
     pl->nq = (pl->tc ? 128 : 16 * pl->rpt) / pl->G;
     const long long RT = (p->Lq + pl->nq - 1) / pl->nq;  // row tiles
     // The tensor-core forward's items are 4, 2 or 1 row tiles (see softmax_tc.cuh).
     // One leaves the fewest SMs idle where all tiles fit them at once; of many, two
     // share the key chunks (long32k: 187 us, four 191, one 237), and four pay once
     // a tile's band is long (8192 dense tokens: 430 us, two 454).
-    const long long W = std::min(p->W, p->Lk);
     pl->nr = 1;
     if (pl->tc && BH * RT > sms) pl->nr = W >= 4096 && BH * RT >= 6LL * sms ? 4 : 2;
     pl->per = pl->nr * pl->nq;
@@ -66,7 +69,7 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     // A few query rows over many keys (single new tokens) would leave most SMs
     // idle: then every tile's keys are cut into parts for about two blocks an
     // SM, of at least four chunks each, joined by a second kernel.
-    const long long keys = std::min<long long>(p->Lk, W + (p->causal ? 0 : W) + pl->per);
+    const long long keys = std::min<long long>(p->Lk, span + pl->per);
     const long long chunks = (keys + 63) / 64;
     pl->nsplit = 1;
     if (tiles > 0 && tiles < sms)
@@ -86,7 +89,17 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     const size_t head = kHeader + align_up((size_t)p->B * 8);
     pl->part_ml = head + align_up((size_t)parts * kD * 4);
     pl->fwd_bytes = pl->part_ml + align_up((size_t)parts * 8);
-    pl->bwd_bytes = head + align_up((size_t)pl->rows * (pl->tc ? 32 : 4));
+    // the fp32 backward's tiles, where few, are cut likewise
+    const long long kchunks = (std::min<long long>(p->Lq, span + 64) + 63) / 64 * pl->G, kt = BH * pl->nktile;
+    pl->qsplit = pl->ksplit = 1;
+    if (!pl->tc && pl->rows > 0 && tiles < sms)
+        pl->qsplit = (int)std::max<long long>(1, std::min(2LL * sms / tiles, chunks / 3));
+    if (!pl->tc && pl->rows > 0 && kt < sms)
+        pl->ksplit = (int)std::max<long long>(1, std::min(2LL * sms / kt, kchunks / 3));
+    const long long qparts = pl->qsplit > 1 ? pl->rows * pl->qsplit * 64 : 0;
+    const long long kparts = pl->ksplit > 1 ? BH * p->Lk * pl->ksplit * 128 : 0;
+    pl->bwd_part = head + align_up((size_t)pl->rows * (pl->tc ? 32 : 4));
+    pl->bwd_bytes = pl->bwd_part + align_up((size_t)std::max(qparts, kparts) * 4);
     return SA_OK;
 }
 
@@ -216,10 +229,18 @@ template <int RPT>
 cudaError_t bwd_simt(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cudaStream_t st) {
     using namespace sm::simt;
     const long long BH = (long long)p->B * p->Hk;
-    const cudaError_t e = launch(k_bwd_q<RPT>, BH * a.ntile, THREADS, smem_bytes(RPT, 3, 2 * nbuf(RPT, true)), st, a);
+    auto sum = [&](long long rows, int kv) {
+        return launch_pdl(k_sum, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, a, kv);
+    };
+    a.nsplit = pl.qsplit;
+    cudaError_t e = launch(k_bwd_q<RPT>, BH * a.ntile * a.nsplit, THREADS, smem_bytes(RPT, 3, 2 * nbuf(RPT, true)), st, a);
+    if (e == cudaSuccess && a.nsplit > 1) e = sum(pl.rows, 0);
     if (e != cudaSuccess) return e;
     a.ntile = pl.nktile;
-    return launch(k_bwd_kv<RPT>, BH * pl.nktile, THREADS, smem_bytes(RPT, 4, 2 * nbuf(RPT, true)), st, a);
+    a.nsplit = pl.ksplit;
+    e = launch(k_bwd_kv<RPT>, BH * a.ntile * a.nsplit, THREADS, smem_bytes(RPT, 4, 2 * nbuf(RPT, true)), st, a);
+    if (e == cudaSuccess && a.nsplit > 1) e = sum(BH * p->Lk, 1);
+    return e;
 }
 
 // The queries' further channels, [rows of B Hq][Lq][16] bf16: boxes of 64
@@ -347,6 +368,7 @@ sa_status sinkhorn_attn_softmax_bwd(const sa_softmax_params* p, const void* q, c
     a.u = const_cast<float*>(u);
     a.D = (float*)((char*)ws + kHeader + align_up((size_t)p->B * 8));
     a.aug = (uint4*)a.D;
+    a.part_o = (float*)((char*)ws + pl.bwd_part);
     // With few keys a row's probabilities are large and dO . O, taken from the
     // rounded O, is off by about as much as the dS it is subtracted in: up to
     // 64 keys the sweep forms D itself, in a pass of its own over them.

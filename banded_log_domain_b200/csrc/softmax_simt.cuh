@@ -266,7 +266,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_q(const Args a) {
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
     RowTile<RPT> rt;
     rt.init(a, ty);
-    const int n = (rt.jhi - rt.jlo + 64) / 64;
+    const int nc = (rt.jhi - rt.jlo + 64) / 64;
+    const int n0 = (int)((long long)nc * rt.part / a.nsplit), n = (int)((long long)nc * (rt.part + 1) / a.nsplit);
     auto qrow = [&](const View& x, int r) -> const T* {
         int h, t;
         if (!rt.row(a, r, h, t)) return nullptr;
@@ -289,7 +290,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_q(const Args a) {
     };
     copy_tile<16 * RPT>(Q, a.q.at<T>(0, 0, 0), [&](int r) { return qrow(a.q, r); });
     copy_tile<16 * RPT>(dO, a.q.at<T>(0, 0, 0), [&](int r) { return qrow(a.dO, r); });
-    if (n > 0) fetch(0);
+    if (n0 < n) fetch(n0);
     else copy_commit();
     float u2[RPT], D[RPT];
     float4 o[RPT];
@@ -308,7 +309,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_q(const Args a) {
         const float4 g = *reinterpret_cast<const float4*>(dO + (ty * RPT + i) * LD + tx * 4);
         D[i] = sum16(fmaf(o[i].x, g.x, fmaf(o[i].y, g.y, fmaf(o[i].z, g.z, o[i].w * g.w))));
     }
-    for (int ch = 0; ch < n; ++ch) {
+    for (int ch = n0; ch < n; ++ch) {
         const int c0 = rt.jlo + 64 * ch, bf = ch % NB;
         const float *K = K0 + 2 * bf * TILE, *V = K + TILE;
         live_keys(a, rt.b, c0, words[ch & 1]);
@@ -340,8 +341,10 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_q(const Args a) {
         float x[4];
         tc::upk2(acc[i][0], x[0], x[1]);
         tc::upk2(acc[i][1], x[2], x[3]);
-        store4(a.dq.at<T>(rt.b, h, t) + tx * 4, x[0] * a.c, x[1] * a.c, x[2] * a.c, x[3] * a.c);
-        if (tx == 0) a.D[((long long)rt.b * a.Hq + h) * a.Lq + t] = D[i];
+        const long long row = ((long long)rt.b * a.Hq + h) * a.Lq + t;
+        T* out = a.nsplit > 1 ? a.part_o + (row * a.nsplit + rt.part) * 64 : a.dq.at<T>(rt.b, h, t);
+        store4(out + tx * 4, x[0] * a.c, x[1] * a.c, x[2] * a.c, x[3] * a.c);
+        if (tx == 0 && rt.part == 0) a.D[row] = D[i];
     }
 }
 
@@ -357,6 +360,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_kv(const Args a) {
     tc::grid_dep_wait();
     tc::grid_dep_launch();
     int x = blockIdx.x;
+    const int part = x % a.nsplit;
+    x /= a.nsplit;
     constexpr int M = 16 * RPT;
     const int j0 = (x % a.ntile) * M;
     x /= a.ntile;
@@ -382,7 +387,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_kv(const Args a) {
 #pragma unroll
     for (int i = 0; i < RPT; ++i) dk[i][0] = dk[i][1] = dv[i][0] = dv[i][1] = 0;
     constexpr int NB = nbuf(RPT, true);
-    const int ny = n * a.G;  // chunks of queries, head after head
+    // chunks of queries, head after head: this part's
+    const int y0 = (int)((long long)n * a.G * part / a.nsplit), ny = (int)((long long)n * a.G * (part + 1) / a.nsplit);
     auto fetch = [&](int y) {
         const int h = hk * a.G + y / n, t0 = (int)il + 64 * (y % n), bf = y % NB;
         if (threadIdx.x < 64) {
@@ -402,8 +408,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_kv(const Args a) {
         copy_tile<64>(Q0 + (2 * bf + 1) * TILE, a.dO.at<T>(0, 0, 0), [&](int r) { return row(a.dO, r); });
         copy_commit();
     };
-    if (ny > 0) fetch(0);
-    for (int y = 0; y < ny; ++y) {
+    if (y0 < ny) fetch(y0);
+    for (int y = y0; y < ny; ++y) {
         const int t0 = (int)il + 64 * (y % n), bf = y % NB;
         const float *Q = Q0 + 2 * bf * TILE, *dO = Q + TILE;
         copy_wait();
@@ -438,10 +444,33 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_kv(const Args a) {
         float z[4];
         tc::upk2(dv[i][0], z[0], z[1]);
         tc::upk2(dv[i][1], z[2], z[3]);
-        store4(a.dv.at<T>(b, hk, j) + tx * 4, z[0], z[1], z[2], z[3]);
+        const long long row = ((long long)b * a.Hk + hk) * a.Lk + j;
+        T* out = a.part_o + (row * a.nsplit + part) * 128;
+        store4((a.nsplit > 1 ? out : a.dv.at<T>(b, hk, j)) + tx * 4, z[0], z[1], z[2], z[3]);
         tc::upk2(dk[i][0], z[0], z[1]);
         tc::upk2(dk[i][1], z[2], z[3]);
-        store4(a.dk.at<T>(b, hk, j) + tx * 4, z[0] * a.c, z[1] * a.c, z[2] * a.c, z[3] * a.c);
+        store4((a.nsplit > 1 ? out + 64 : a.dk.at<T>(b, hk, j)) + tx * 4, z[0] * a.c, z[1] * a.c, z[2] * a.c, z[3] * a.c);
+    }
+}
+
+// The parts' gradients added up in their order, one warp per row: dQ, or dV and dK.
+__global__ void __launch_bounds__(128) k_sum(const Args a, int kv) {
+    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, H = kv ? a.Hk : a.Hq, L = kv ? a.Lk : a.Lq;
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
+    if (row >= (long long)a.B * H * L) return;
+    const int t = (int)(row % L), h = (int)(row / L % H), b = (int)(row / L / H);
+    for (int z = 0; z < (kv ? 2 : 1); ++z) {
+        const float2* p = reinterpret_cast<const float2*>(a.part_o + row * a.nsplit * (kv ? 128 : 64) + 64 * z) + lane;
+        float2 s = make_float2(0.f, 0.f);
+#pragma unroll 4
+        for (int i = 0; i < a.nsplit; ++i) {
+            const float2 x = p[i * (kv ? 64 : 32)];
+            s.x += x.x;
+            s.y += x.y;
+        }
+        reinterpret_cast<float2*>((!kv ? a.dq : z == 0 ? a.dv : a.dk).at<float>(b, h, t))[lane] = s;
     }
 }
 
