@@ -145,7 +145,8 @@ sa_status rotary_call(const sa_rotary_params* p, const double* freqs, const int*
     if (p->interleaved != 0 && p->interleaved != 1) return SA_ERR_INVALID_ARG;
     if (p->dtype != SA_F32 && p->dtype != SA_BF16) return SA_ERR_INVALID_ARG;
     if (!std::isfinite(p->scale)) return SA_ERR_INVALID_ARG;
-    if (p->d % 8 || p->d > 256 || p->B > 65535 || (long long)p->Hq + p->Hk > 65535) return SA_ERR_UNSUPPORTED;
+    if (p->d % 8 || p->d > 256 || p->B > 65535 || (long long)p->Hq + p->Hk > 65535 || p->L > (1 << 30))
+        return SA_ERR_UNSUPPORTED;  // (token indices stay clear of 2^31 with a block's rows added)
     const int size = p->dtype == SA_F32 ? 4 : 2;
     RotArgs a;
     if (!strides(p->q_stride, p->B, p->Hq, p->L, p->d, size, a.qs) ||

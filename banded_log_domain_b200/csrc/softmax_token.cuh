@@ -52,7 +52,12 @@ struct Line {
         return __reduce_add_sync(~0u, n);
     }
 };
-// Block i of n takes chunks [total i / n, total (i + 1) / n).
+// Block i of n takes chunks [total i / n, total (i + 1) / n); n is the number of
+// blocks, or of chunks where there are fewer (no share is then empty, and every
+// block between a pair's first and last has written its part).
+__device__ __forceinline__ int share_count(long long total, int blocks) {
+    return (int)(total < blocks ? total : blocks);
+}
 __device__ __forceinline__ long long share_begin(long long total, int i, int n) { return total * i / n; }
 __device__ __forceinline__ int share_of(long long chunk, long long total, int n) {
     return (int)(((chunk + 1) * n - 1) / total);
@@ -79,12 +84,13 @@ struct Share {
     bool whole = false;
     __device__ explicit Share(const Args& a) {  // the whole block calls
         const long long total = Line::before(a, a.B) * a.Hk;
-        at = share_begin(total, blockIdx.x, gridDim.x);
-        end = share_begin(total, blockIdx.x + 1, gridDim.x);
+        const int n = share_count(total, gridDim.x), i = blockIdx.x;
+        at = i < n ? share_begin(total, i, n) : 0;
+        end = i < n ? share_begin(total, i + 1, n) : 0;
         if (at < end && !ragged(a)) {
-            const long long n = (long long)Line::chunks(a, 0) * a.Hk;
-            b = (int)(at / n);
-            start = b * n;
+            const long long len = (long long)Line::chunks(a, 0) * a.Hk;
+            b = (int)(at / len);
+            start = b * len;
         }
     }
     __device__ bool next(const Args& a) {
@@ -555,8 +561,9 @@ __global__ void __launch_bounds__(128) k_token_join(const Args a, int nblocks) {
     int i0 = 0, i1 = -1;
     if (n > 0) {
         const long long s = Line::before(a, b) * a.Hk + (long long)hk * n;
-        i0 = share_of(s, total, nblocks);
-        i1 = share_of(s + n - 1, total, nblocks);
+        const int shares = share_count(total, nblocks);
+        i0 = share_of(s, total, shares);
+        i1 = share_of(s + n - 1, total, shares);
         if (i0 == i1) return;  // one block had all of it
     }
     float m = -INFINITY, l = 0.f;

@@ -22,7 +22,7 @@
  *   constant score dustbin_score, with unit mass like every other row/column.
  *
  * Debug build: compiled with -DSA_DEBUG (libsinkhorn_attn_debug.so) every
- * kernel checks the indices of its guarded accesses (global rows and columns,
+ * kernel of the Sinkhorn attention checks the indices of its guarded accesses (global rows and columns,
  * ring and buffer slots, tensor-memory columns, shared-memory offsets) before
  * making them; a failed check skips the access and records SA_ERR_BOUNDS in
  * the status word (read by sinkhorn_attn_poll).  Nothing traps.
@@ -386,7 +386,7 @@ sa_status sinkhorn_attn_bias_certificate(int n_depths, const int* depths, int n_
  *     element strides for batch, head and token (x_stride; three zeros:
  *     contiguous; the stride of an extent of 1 is not read), positive
  *     multiples of 16 bytes, d contiguous.  Tensors written must not overlap
- *     themselves or each other.  u is contiguous [B][Hq][Lq].
+ *     themselves or any other tensor of the call.  u is contiguous [B][Hq][Lq].
  *   - The contents of masked tokens, and of keys outside every band of the call
  *     (the unwritten tail of a cache), are not used, whatever they hold.  A
  *     non-finite value of a token in use reaches the rows that attend it and
@@ -397,7 +397,8 @@ sa_status sinkhorn_attn_bias_certificate(int n_depths, const int* depths, int n_
  *     at once, or captured into graphs that may run at once, need one each.
  */
 typedef struct {
-    int B, Hq, Hk, Lq, Lk, d;  /* d == 64, Hq a multiple of Hk, Hq / Hk <= 64, Lq <= Lk */
+    int B, Hq, Hk, Lq, Lk, d;  /* d == 64, Hq a multiple of Hk, Hq / Hk <= 64,
+                                  B Hq <= 65535, Lq <= Lk <= 2^30 */
     int W;                     /* band half-width, W >= 0 (W >= Lk - 1 is dense) */
     float eps;                 /* temperature, > 0 */
     int causal;                /* 0 or 1: keys at later positions are left out */
@@ -406,10 +407,10 @@ typedef struct {
     long long dO_stride[3], dq_stride[3], dk_stride[3], dv_stride[3];
 } sa_softmax_params;
 
-/* Workspace bytes of the two calls below (either pointer may be NULL).  The
- * forward's holds partial rows where few queries have their keys split over
- * several blocks (at most 37 MB); the backward's 4 (fp32) or 32 (bf16) bytes per
- * query row; both 8 bytes per sequence. */
+/* Workspace bytes of the two calls below (either pointer may be NULL).  Both hold
+ * 8 bytes per sequence; the backward's 4 (fp32) or 32 (bf16) bytes per query row;
+ * and where few rows have their keys split over several blocks, the parts: at
+ * most 37 MB in the forward, 10 MB in the fp32 backward. */
 sa_status sinkhorn_attn_softmax_workspace_size(const sa_softmax_params* p, size_t* fwd_bytes,
                                                size_t* bwd_bytes);
 
@@ -444,7 +445,8 @@ sa_status sinkhorn_attn_softmax_bwd(const sa_softmax_params* p, const void* q, c
  *   - k, k_out may be NULL when Hk == 0 (queries alone).
  */
 typedef struct {
-    int B, Hq, Hk, L, d;       /* d a multiple of 8, at most 256; Hk >= 0 */
+    int B, Hq, Hk, L, d;       /* d a multiple of 8, at most 256; Hk >= 0; B and
+                                  Hq + Hk <= 65535, L <= 2^30 */
     int rot;                   /* leading channels that are turned, even, 2 <= rot <= d */
     int interleaved;           /* 0 or 1 */
     float scale;               /* finite */

@@ -77,6 +77,13 @@ def test_workspace_is_bounded_and_grows_with_the_rows_only():
         for B in (1, 3, 64, 147):
             f, _ = sa.sinkhorn_attn_softmax_workspace_size(P(B=B, Hq=64, Hk=1, Lq=1, Lk=Lk, W=Lk))
             assert f <= 37 << 20
+    for dt in (sa.SA_F32, sa.SA_BF16):
+        for Lq in (1, 8, 100, 1000, 4000):
+            for H in (1, 8, 100):
+                q = P(B=1, Hq=H, Hk=H, Lq=Lq, Lk=1 << 20, W=1 << 20, dtype=dt)
+                f, b = sa.sinkhorn_attn_softmax_workspace_size(q)
+                rows = 512 + (H * Lq * (32 if dt == sa.SA_BF16 else 4) + 255) // 256 * 256
+                assert f <= 37 << 20 and rows <= b <= rows + (10 << 20)
     f, b = sa.sinkhorn_attn_softmax_workspace_size(P(B=1, Hq=16, Hk=16, Lq=32768, Lk=32768, W=256))
     assert f == 512 and b == 512 + 16 * 32768 * 32
 
@@ -85,6 +92,7 @@ def test_workspace_is_bounded_and_grows_with_the_rows_only():
     (dict(B=-1), -1), (dict(L=-1), -1), (dict(rot=0), -1), (dict(rot=63), -1), (dict(rot=66), -1),
     (dict(interleaved=2), -1), (dict(dtype=9), -1), (dict(scale=float("inf")), -1),
     (dict(d=68, rot=64), -2), (dict(d=264, rot=64), -2), (dict(B=65536), -2), (dict(Hq=65536), -2),
+    (dict(L=(1 << 30) + 1), -2),
     (dict(), -1),  # null pointers
 ])
 def test_rotary_refuses(kw, status):

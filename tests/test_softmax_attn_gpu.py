@@ -140,6 +140,32 @@ def test_strided_tensors(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+def test_offsets_beyond_32_bits(dtype):
+    # a cache whose tokens lie 2^17 elements apart: the last ones are past 2^31 elements
+    import banded_log_domain_b200 as sa
+
+    L = 17000
+    q, k, v, dO = draw(dtype, 1, 2, 1, 200, L, seed=11)
+    big = torch.empty(L << 17, dtype=dtype, device="cuda")
+    kb = big.as_strided((1, 1, L, 64), (L << 17, L << 17, 1 << 17, 1))
+    vb = big.as_strided((1, 1, L, 64), (L << 17, L << 17, 1 << 17, 1), 64)
+    kb.copy_(k)
+    vb.copy_(v)
+    for n in (1, 200):  # single tokens, and tiles
+        kw = dict(W=300, causal=True)
+        o, u = sa.sinkhorn_attn_softmax_fwd(q[:, :, 200 - n:], kb, vb, **kw)
+        wo, wu = sa.sinkhorn_attn_softmax_fwd(q[:, :, 200 - n:], k, v, **kw)
+        assert torch.equal(o, wo) and torch.equal(u, wu)
+    g = sa.sinkhorn_attn_softmax_bwd(q, kb, vb, o, dO, u, **kw)
+    assert all(torch.equal(x, y) for x, y in zip(g, sa.sinkhorn_attn_softmax_bwd(q, k, v, o, dO, u, **kw)))
+    freqs, _ = sa.sinkhorn_attn_rotary_freqs(64)
+    r, _ = sa.sinkhorn_attn_rotary_fwd(kb, None, freqs)
+    assert torch.equal(r, sa.sinkhorn_attn_rotary_fwd(k, None, freqs)[0])
+    sa.sinkhorn_attn_rotary_fwd(kb, None, freqs, q_out=vb)
+    assert torch.equal(vb, r)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_a_longer_problem_and_a_head_of_it(dtype):
     # The bounds of the whole and of one key head with its two query heads alone.  The
     # two need not be equal to the bit: how many row tiles share an item, and with
@@ -203,6 +229,42 @@ def test_same_results_again_in_a_graph_and_on_two_streams(dtype):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, w))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("Lq,Lk,H", [(4, 40000, 1), (16, 20000, 1), (70, 9000, 2), (300, 3000, 1), (1100, 1100, 1)])
+def test_split_keys_of_few_rows(dtype, Lq, Lk, H):
+    # the parts of a row's keys, forward and (fp32) backward; where most tokens are
+    # masked there are fewer chunks than blocks
+    q, k, v, dO = draw(dtype, 1, H, H, Lq, Lk, seed=Lq)
+    check(q, k, v, dO, W=Lk)
+    mask = torch.ones(1, Lk, dtype=torch.uint8, device="cuda")
+    mask[:, :Lk - Lq - 100] = 0
+    for _ in range(3):  # workspaces that held other parts
+        check(q, k, v, dO, W=Lk, mask=mask, causal=True)
+        check(q, k, v, dO, W=Lk, mask=mask)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("Hq,Hk,Lq,Lk,W,masked", [(2, 1, 1, 5000, 5000, False), (2, 1, 2, 5000, 5000, True),
+                                                  (8, 1, 3, 700, 30, True), (4, 1, 40, 3000, 3000, False),
+                                                  (2, 2, 300, 900, 900, True), (2, 2, 500, 500, 20, False)])
+def test_a_workspace_may_hold_anything(dtype, Hq, Hk, Lq, Lk, W, masked):
+    import banded_log_domain_b200 as sa
+
+    q, k, v, dO = draw(dtype, 2, Hq, Hk, Lq, Lk, seed=Lq)
+    mask = (torch.rand(2, Lk, generator=torch.Generator("cuda").manual_seed(2), device="cuda") < 0.05).to(torch.uint8)
+    kw = dict(W=W, mask=mask if masked else None, q_pos=torch.tensor([Lk - Lq, Lk // 7], dtype=torch.int32, device="cuda"))
+    p = sa._softmax_params(q, k, v, W, 1.0, False)
+    f, b = sa.sinkhorn_attn_softmax_workspace_size(p)
+    got = []
+    for fill in (0, 0xff):  # zeros, and NaN
+        ws = torch.full((max(f, b),), fill, dtype=torch.uint8, device="cuda")
+        o, u = sa.sinkhorn_attn_softmax_fwd(q, k, v, ws=ws, **kw)
+        ws.fill_(fill)
+        got.append((o, u) + sa.sinkhorn_attn_softmax_bwd(q, k, v, o, dO, u, ws=ws, **kw))
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+    assert all(bool(torch.isfinite(x).all()) for x in got[0])
 
 
 def test_workspace_status_and_reuse():
