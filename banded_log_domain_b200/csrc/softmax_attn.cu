@@ -7,6 +7,7 @@
 #include "host_util.cuh"
 #include "softmax.cuh"
 #include "softmax_simt.cuh"
+#include "softmax_tf32.cuh"
 #include "softmax_tc.cuh"
 #include "softmax_tc_bwd.cuh"
 #include "softmax_token.cuh"
@@ -47,9 +48,9 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     const int sms = sm_count();
     const long long BH = (long long)p->B * p->Hk;
     const long long W = std::min(p->W, p->Lk), span = W + (p->causal ? 0 : W);
-    // fp32 tiles of 64 rows; of 32 or 16, which read more shared memory per
-    // product, where even those find an SM each and a row's keys are too few to
-    // be cut into parts instead
+    // fp32 tiles of 64 rows on matrix instructions (softmax_tf32.cuh); of 32 or 16
+    // on the FMA pipe (softmax_simt.cuh) where even those find an SM each and a
+    // row's keys are too few to be cut into parts instead
     const long long t64 = BH * ((p->Lq + 64 / pl->G - 1) / (64 / pl->G));
     const bool few = span <= 384;
     pl->rpt = few && pl->G <= 16 && 4 * t64 <= sms ? 1 : few && pl->G <= 32 && 2 * t64 <= sms ? 2 : 4;
@@ -157,11 +158,37 @@ void base_args(sm::Args* a, const sa_softmax_params* p, const Plan& pl, const ui
     a->exact_d = 0;
 }
 
-template <int RPT>
-cudaError_t fwd_simt(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
-    const long long tiles = (long long)p->B * p->Hk * pl.ntile;
-    return launch(sm::simt::k_fwd<RPT>, tiles * pl.nsplit, sm::simt::THREADS, sm::simt::smem_bytes(RPT, 2, 2 * sm::simt::nbuf(RPT, false)), st,
+cudaError_t fwd_f32(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
+    namespace simt = sm::simt;
+    const long long grid = (long long)p->B * p->Hk * pl.ntile * pl.nsplit;
+    if (pl.rpt == 4) return launch(sm::tf32::k_fwd, grid, sm::tf32::THREADS, sm::tf32::smem_bytes(5), st, a);
+    return launch(pl.rpt == 2 ? simt::k_fwd<2> : simt::k_fwd<1>, grid, simt::THREADS, simt::smem_bytes(pl.rpt, 2, 4), st,
                   a);
+}
+
+// One sweep of the fp32 backward: dQ, or dK and dV.
+cudaError_t sweep_f32(int rpt, bool kv, long long grid, const sm::Args& a, cudaStream_t st) {
+    namespace simt = sm::simt;
+    namespace tf32 = sm::tf32;
+    if (rpt == 4) return launch(kv ? tf32::k_bwd_kv : tf32::k_bwd_q, grid, tf32::THREADS, tf32::smem_bytes(6), st, a);
+    auto kern = kv ? (rpt == 2 ? simt::k_bwd_kv<2> : simt::k_bwd_kv<1>) : (rpt == 2 ? simt::k_bwd_q<2> : simt::k_bwd_q<1>);
+    return launch(kern, grid, simt::THREADS, simt::smem_bytes(rpt, kv ? 4 : 3, 4), st, a);
+}
+
+cudaError_t bwd_f32(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cudaStream_t st) {
+    const long long BH = (long long)p->B * p->Hk;
+    auto sum = [&](long long rows, int kv) {
+        return launch_pdl(sm::simt::k_sum, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, a, kv);
+    };
+    a.nsplit = pl.qsplit;
+    cudaError_t e = sweep_f32(pl.rpt, false, BH * a.ntile * a.nsplit, a, st);
+    if (e == cudaSuccess && a.nsplit > 1) e = sum(pl.rows, 0);
+    if (e != cudaSuccess) return e;
+    a.ntile = pl.nktile;
+    a.nsplit = pl.ksplit;
+    e = sweep_f32(pl.rpt, true, BH * a.ntile * a.nsplit, a, st);
+    if (e == cudaSuccess && a.nsplit > 1) e = sum(BH * p->Lk, 1);
+    return e;
 }
 
 // A [B][H][L][64] bf16 view as a 4-D tensor; boxes of `tokens` x `heads` rows.
@@ -215,32 +242,12 @@ cudaError_t fwd_token(const sa_softmax_params* p, const Plan& pl, const sm::Args
 
 cudaError_t fwd_launch(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
     if (pl.token) return fwd_token(p, pl, a, st);
-    const cudaError_t e = !pl.tc         ? (pl.rpt == 4   ? fwd_simt<4>(p, pl, a, st)
-                                          : pl.rpt == 2 ? fwd_simt<2>(p, pl, a, st)
-                                                        : fwd_simt<1>(p, pl, a, st))
+    const cudaError_t e = !pl.tc       ? fwd_f32(p, pl, a, st)
                           : pl.nr == 4 ? fwd_tc<4>(p, pl, a, st)
                           : pl.nr == 2 ? fwd_tc<2>(p, pl, a, st)
                                        : fwd_tc<1>(p, pl, a, st);
     if (e != cudaSuccess || pl.nparts == 1) return e;
     return launch(pl.tc ? sm::k_join<__nv_bfloat16> : sm::k_join<float>, (pl.rows + 3) / 4, 128, 0, st, a);
-}
-
-template <int RPT>
-cudaError_t bwd_simt(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cudaStream_t st) {
-    using namespace sm::simt;
-    const long long BH = (long long)p->B * p->Hk;
-    auto sum = [&](long long rows, int kv) {
-        return launch_pdl(k_sum, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st, a, kv);
-    };
-    a.nsplit = pl.qsplit;
-    cudaError_t e = launch(k_bwd_q<RPT>, BH * a.ntile * a.nsplit, THREADS, smem_bytes(RPT, 3, 2 * nbuf(RPT, true)), st, a);
-    if (e == cudaSuccess && a.nsplit > 1) e = sum(pl.rows, 0);
-    if (e != cudaSuccess) return e;
-    a.ntile = pl.nktile;
-    a.nsplit = pl.ksplit;
-    e = launch(k_bwd_kv<RPT>, BH * a.ntile * a.nsplit, THREADS, smem_bytes(RPT, 4, 2 * nbuf(RPT, true)), st, a);
-    if (e == cudaSuccess && a.nsplit > 1) e = sum(BH * p->Lk, 1);
-    return e;
 }
 
 // The queries' further channels, [rows of B Hq][Lq][16] bf16: boxes of 64
@@ -285,10 +292,7 @@ cudaError_t zero_grads(const sa_softmax_params* p, sm::Args& a, cudaStream_t st)
 }
 
 cudaError_t bwd_launch(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cudaStream_t st) {
-    if (!pl.tc)
-        return pl.rpt == 4   ? bwd_simt<4>(p, pl, a, st)
-               : pl.rpt == 2 ? bwd_simt<2>(p, pl, a, st)
-                             : bwd_simt<1>(p, pl, a, st);
+    if (!pl.tc) return bwd_f32(p, pl, a, st);
     const long long BH = (long long)p->B * p->Hk;
     a.nq = pl.nq;
     a.ntile = (p->Lq + a.nq - 1) / a.nq;

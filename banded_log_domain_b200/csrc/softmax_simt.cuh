@@ -1,8 +1,8 @@
-// Softmax attention on the FP32 pipe (fp32 storage): tiles of 16 RPT rows x 64
-// columns, 256 threads of RPT x 4 entries.  All products are packed f32x2 FMAs on
-// operands in shared memory; bound by FFMA issue and the shared-memory reads that
-// feed it.  RPT is 4; 2 or 1 where the tiles are few (the 512-token problem's
-// three kernels: 98 us with 4, 50 with 1).
+// Softmax attention on the FP32 pipe, for fp32 problems of few small tiles: 16 RPT
+// rows x 64 columns (RPT 1 or 2), 256 threads of RPT x 4 entries.  All products are
+// packed f32x2 FMAs on operands in shared memory, bound by the shared-memory
+// reads; what counts here is the latency of a tile's short chain of chunks (the
+// 512-token problem's three kernels: 98 us with 64 rows a tile, 50 with 16).
 #pragma once
 
 #include "softmax.cuh"
@@ -20,9 +20,6 @@ constexpr int TILE = 64 * LD;
 __host__ __device__ constexpr int rtile(int rpt) { return 16 * rpt * LD; }
 // bytes of `r` row tiles and `c` chunk tiles
 __host__ __device__ constexpr int smem_bytes(int rpt, int r, int c) { return (r * rtile(rpt) + c * TILE) * 4; }
-// chunk buffers: two, the next chunk's copies in flight during this one's
-// products, where two blocks still fit an SM
-__host__ __device__ constexpr int nbuf(int rpt, bool bwd) { return bwd && rpt == 4 ? 1 : 2; }
 
 // s[i][j] = sum_k A[ty * RPT + i][k] B[tx + 16 j][k] (even and odd k apart, then together)
 template <int RPT>
@@ -181,9 +178,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_fwd(const Args a) {
         l[i] = 0.f;
         o[i][0] = o[i][1] = 0;
     }
-    constexpr int NB = nbuf(RPT, false);
     auto fetch = [&](int ch) {
-        const int c0 = rt.jlo + 64 * ch, bf = ch % NB;
+        const int c0 = rt.jlo + 64 * ch, bf = ch & 1;
         auto row = [&](const View& x, int r) -> const T* {
             const int j = c0 + r;
             return j <= rt.jhi && a.live(rt.b, j) ? x.at<T>(rt.b, rt.hk, j) : nullptr;
@@ -194,7 +190,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_fwd(const Args a) {
     };
     if (n0 < n1) fetch(n0);
     for (int ch = n0; ch < n1; ++ch) {
-        const int c0 = rt.jlo + 64 * ch, bf = ch % NB;
+        const int c0 = rt.jlo + 64 * ch, bf = ch & 1;
         const float *K = K0 + 2 * bf * TILE, *V = K + TILE;
         live_keys(a, rt.b, c0, words[ch & 1]);
         copy_wait();
@@ -277,9 +273,8 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_q(const Args a) {
     uint64_t acc[RPT][2];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) acc[i][0] = acc[i][1] = 0;
-    constexpr int NB = nbuf(RPT, true);
     auto fetch = [&](int ch) {
-        const int c0 = rt.jlo + 64 * ch, bf = ch % NB;
+        const int c0 = rt.jlo + 64 * ch, bf = ch & 1;
         auto row = [&](const View& x, int r) -> const T* {
             const int j = c0 + r;
             return j <= rt.jhi && a.live(rt.b, j) ? x.at<T>(rt.b, rt.hk, j) : nullptr;
@@ -310,12 +305,12 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_q(const Args a) {
         D[i] = sum16(fmaf(o[i].x, g.x, fmaf(o[i].y, g.y, fmaf(o[i].z, g.z, o[i].w * g.w))));
     }
     for (int ch = n0; ch < n; ++ch) {
-        const int c0 = rt.jlo + 64 * ch, bf = ch % NB;
+        const int c0 = rt.jlo + 64 * ch, bf = ch & 1;
         const float *K = K0 + 2 * bf * TILE, *V = K + TILE;
         live_keys(a, rt.b, c0, words[ch & 1]);
         copy_wait();
         __syncthreads();
-        if (NB == 2 && ch + 1 < n) fetch(ch + 1);
+        if (ch + 1 < n) fetch(ch + 1);
         float s[RPT][4], g[RPT][4];
         mm_abt<RPT>(Q, K, ty, tx, s);
         mm_abt<RPT>(dO, V, ty, tx, g);
@@ -329,10 +324,6 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_q(const Args a) {
             }
         __syncwarp();  // a warp writes and reads the same rows of S
         mm_ab<RPT>(S, K, ty, tx, acc);
-        if (NB == 1 && ch + 1 < n) {
-            __syncthreads();
-            fetch(ch + 1);
-        }
     }
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
@@ -386,11 +377,10 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_kv(const Args a) {
     uint64_t dk[RPT][2], dv[RPT][2];
 #pragma unroll
     for (int i = 0; i < RPT; ++i) dk[i][0] = dk[i][1] = dv[i][0] = dv[i][1] = 0;
-    constexpr int NB = nbuf(RPT, true);
     // chunks of queries, head after head: this part's
     const int y0 = (int)((long long)n * a.G * part / a.nsplit), ny = (int)((long long)n * a.G * (part + 1) / a.nsplit);
     auto fetch = [&](int y) {
-        const int h = hk * a.G + y / n, t0 = (int)il + 64 * (y % n), bf = y % NB;
+        const int h = hk * a.G + y / n, t0 = (int)il + 64 * (y % n), bf = y & 1;
         if (threadIdx.x < 64) {
             const int t = t0 + threadIdx.x;
             const bool on = t <= ih && a.live(b, (int)(first + t));
@@ -410,11 +400,11 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_kv(const Args a) {
     };
     if (y0 < ny) fetch(y0);
     for (int y = y0; y < ny; ++y) {
-        const int t0 = (int)il + 64 * (y % n), bf = y % NB;
+        const int t0 = (int)il + 64 * (y % n), bf = y & 1;
         const float *Q = Q0 + 2 * bf * TILE, *dO = Q + TILE;
         copy_wait();
         __syncthreads();
-        if (NB == 2 && y + 1 < ny) fetch(y + 1);
+        if (y + 1 < ny) fetch(y + 1);
         float s[RPT][4], g[RPT][4];
         mm_abt<RPT>(K, Q, ty, tx, s);
         mm_abt<RPT>(V, dO, ty, tx, g);
@@ -432,10 +422,6 @@ __global__ void __launch_bounds__(THREADS, 2) k_bwd_kv(const Args a) {
         __syncwarp();
         mm_ab<RPT>(P, dO, ty, tx, dv);
         mm_ab<RPT>(S, Q, ty, tx, dk);
-        if (NB == 1 && y + 1 < ny) {
-            __syncthreads();
-            fetch(y + 1);
-        }
     }
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
