@@ -1,15 +1,17 @@
 // Softmax attention in fp32 on warp matrix instructions (the larger problems; see
 // softmax_simt.cuh for the few small tiles).
 //
-// Every fp32 operand is split in two tf32 numbers, x = hi + lo (both rounded
-// to nearest 11 bits: 2^-23 of x is lost), and every product is
-// hi lo' + lo hi' + hi hi' with fp32 sums; the cross terms are summed apart.  The
-// terms left out are 2^-22 of a product, so the results stay at fp32's own
-// rounding (3e-7 to 6e-7 against 64 bits, as on the FMA pipe).  mma.sync takes 508
-// tf32 FMA per clock and SM, a third of that here, where the FMA pipe's 128 are
-// halved by the shared-memory reads that feed it: masked2k's training step 0.59 ms
-// on the FMA pipe.  (tcgen05 would take its operands from shared memory in tf32
-// too, but with the splits written back there first, six tiles for two.)
+// Every fp32 operand is split in two tf32 numbers, x = hi + lo, hi rounded to
+// nearest and lo, of either sign, cut to 11 bits (at most 2^-21 of x is lost).
+// Every product is hi lo' + lo hi' + hi hi' with fp32 sums, the cross terms summed
+// apart; the term left out is 2^-22 of a product.  Against 64 bits the results are
+// off by 3e-7 to 7e-7, as on the FMA pipe (6e-7).
+// mma.sync takes 508 tf32 FMA per clock and SM, a third of that here; two warps a
+// scheduler and the splitting keep it half busy.  Measured against 64 x 64 tiles on
+// the FMA pipe, which shared-memory reads hold at 45 % of its rate: masked2k's
+// training step 0.59 ms (0.66), 4096 dense tokens of 4 heads 0.49 + 1.56 ms (0.55 +
+// 1.87).  (tcgen05 takes tf32 operands from shared memory: the splits would have to
+// be written back there first, four tiles for two.)
 //
 // Blocks of four warps, 16 rows each, on tiles of 64 rows x 64 columns.  A lane
 // holds rows g and g + 8, columns 2t and 2t + 1 of every eight (g = lane / 4, t =
@@ -37,22 +39,30 @@ struct Two {
 __device__ __forceinline__ Two split(float x) {
     Two s;
     s.hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-    s.lo = (__float_as_uint(x - __uint_as_float(s.hi)) + 0x1000u) & 0xffffe000u;
+    s.lo = __float_as_uint(x - __uint_as_float(s.hi));  // the instruction reads its upper 19 bits
     return s;
 }
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// c (main), x (cross terms) += a b
-__device__ __forceinline__ void mma3(float (&c)[4], float (&x)[4], const uint32_t (&ah)[4], const uint32_t (&al)[4],
-                                     float b0, float b1) {
-    const Two p = split(b0), q = split(b1);
-    mma(x, al, p.hi, q.hi);
-    mma(x, ah, p.lo, q.lo);
-    mma(c, ah, p.hi, q.hi);
+// c (main), x (cross terms) += a b for four tiles of columns, one kind of product
+// after the other: an accumulator's next use lies four instructions on.
+__device__ __forceinline__ void mma3(float (&c)[4][4], float (&x)[4][4], const uint32_t (&ah)[4],
+                                     const uint32_t (&al)[4], const float (&b0)[4], const float (&b1)[4]) {
+    Two p[4], q[4];
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        p[n] = split(b0[n]);
+        q[n] = split(b1[n]);
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) mma(x[n], al, p[n].hi, q[n].hi);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) mma(c[n], ah, p[n].hi, q[n].hi);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) mma(x[n], ah, p[n].lo, q[n].lo);
 }
 
 // s[n] = A B^T for this warp's 16 rows (A at its first) and the 64 rows of B
@@ -73,11 +83,14 @@ __device__ __forceinline__ void mm_abt(const float* A, const float* B, int g, in
                 ah[e] = y.hi;
                 al[e] = y.lo;
             }
+            float b0[4], b1[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const float* b = B + (32 * h + 8 * n + g) * LD + k + t;
-                mma3(c[n], x[n], ah, al, b[0], b[4]);
+                b0[n] = b[0];
+                b1[n] = b[4];
             }
+            mma3(c, x, ah, al, b0, b1);
         }
 #pragma unroll
         for (int n = 0; n < 4; ++n)
@@ -104,11 +117,14 @@ __device__ __forceinline__ void mm_ab(const float (&p)[8][4], const float* X, in
                 ah[e] = y.hi;
                 al[e] = y.lo;
             }
+            float b0[4], b1[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const float* b = X + (8 * k + 2 * t) * LD + 32 * h + 8 * n + g;
-                mma3(c[n], x[n], ah, al, b[0], b[LD]);
+                b0[n] = b[0];
+                b1[n] = b[LD];
             }
+            mma3(c, x, ah, al, b0, b1);
         }
 #pragma unroll
         for (int n = 0; n < 4; ++n)
