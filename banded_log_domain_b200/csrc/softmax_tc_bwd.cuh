@@ -424,6 +424,24 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             total = (sh[r] + sh[128 + r]) + (sh[256 + r] + sh[384 + r]);
             return true;
         };
+        // DQ: u and O of this thread's row of an item, asked for while the item before ends.
+        float un = 0.f;
+        uint4 orow[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        bool in = false;
+        auto ask = [&](const Item& w) {
+            const int i = w.r0 + iq;
+            const long long p = w.first + i;
+            in = g < a.G && i < a.Lq && p >= 0 && p < a.Lk && a.live(w.b, (int)p);
+            if (!in) return;
+            const int h = w.hk * a.G + g;
+            un = a.u[((long long)w.b * a.Hq + h) * a.Lq + i];
+            if (!EXACT) {
+                const uint4* po = reinterpret_cast<const uint4*>(a.o.at<__nv_bfloat16>(w.b, h, i) + 16 * q4);
+                orow[0] = po[0];
+                orow[1] = po[1];
+            }
+        };
+        if (MODE == DQ && begin_item(0)) ask(items[0]);
         for (int it = 0; ok && begin_item(it); ++it) {
             const Item& w = items[it % NIT];
             const int rb = it & 1, n = w.n, nu = n * passes;
@@ -434,23 +452,11 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             const bool exists = MODE == DQ ? g < a.G && i < a.Lq : i < a.Lk;
             const long long at = MODE == DQ ? ((long long)w.b * a.Hq + w.hk * a.G + g) * a.Lq + i : 0;
             if (MODE == DQ) {
-                uint4 o[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-                bool in = false;
-                if (exists) {
-                    const long long p = w.first + i;
-                    if (p >= 0 && p < a.Lk && a.live(w.b, (int)p)) {
-                        in = true;
-                        a.keys(p, lo, hi);
-                        lo -= w.c0;
-                        hi -= w.c0;
-                        ur = a.u[at] * uscale;
-                        if (!EXACT) {
-                            const uint4* po = reinterpret_cast<const uint4*>(
-                                a.o.at<__nv_bfloat16>(w.b, w.hk * a.G + g, i) + 16 * q4);
-                            o[0] = po[0];
-                            o[1] = po[1];
-                        }
-                    }
+                if (in) {
+                    a.keys(w.first + i, lo, hi);
+                    lo -= w.c0;
+                    hi -= w.c0;
+                    ur = un * uscale;
                 }
                 if (!ctl.wait_warp(RFULL + rb, (it >> 1) & 1)) break;
                 if (!EXACT) {  // D = dO . O, a quarter of the channels here
@@ -459,7 +465,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const uint4 y = *reinterpret_cast<const uint4*>(dO + tc::sw128_off(r, 2 * q4 + e));
-                        const __nv_bfloat162* po = reinterpret_cast<const __nv_bfloat162*>(&o[e]);
+                        const __nv_bfloat162* po = reinterpret_cast<const __nv_bfloat162*>(&orow[e]);
                         const __nv_bfloat162* py = reinterpret_cast<const __nv_bfloat162*>(&y);
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
@@ -570,6 +576,14 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             }
             if (!ok) break;
             gu += nu;
+            if (MODE == DQ && exists && q4 == 0) {  // for the key sweep: u / c and -D
+                uint32_t u0, u1, u2, d0, d1, d2;
+                split3(ur, u0, u1, u2);
+                split3(-D, d0, d1, d2);
+                a.aug[2 * at] = make_uint4(u0 | u1 << 16, u2 | d0 << 16, d1 | d2 << 16, 0u);
+                a.aug[2 * at + 1] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (MODE == DQ && begin_item(it + 1)) ask(items[(it + 1) % NIT]);
             // the accumulators: this warp's lanes, 16 columns
             if (nu > 0) {
                 if (!ctl.wait_warp(ACCFULL, na & 1)) break;
@@ -607,13 +621,6 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bar + ACCEMPTY);
-            }
-            if (MODE == DQ && exists && q4 == 0) {  // for the key sweep: u / c and -D
-                uint32_t u0, u1, u2, d0, d1, d2;
-                split3(ur, u0, u1, u2);
-                split3(-D, d0, d1, d2);
-                a.aug[2 * at] = make_uint4(u0 | u1 << 16, u2 | d0 << 16, d1 | d2 << 16, 0u);
-                a.aug[2 * at + 1] = make_uint4(0u, 0u, 0u, 0u);
             }
             end_item(it);
         }
