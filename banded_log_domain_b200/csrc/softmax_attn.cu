@@ -49,17 +49,20 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     const long long BH = (long long)p->B * p->Hk;
     const long long W = std::min(p->W, p->Lk), span = W + (p->causal ? 0 : W);
     // fp32 tiles of 64 rows on matrix instructions (softmax_tf32.cuh); of 32 or 16
-    // on the FMA pipe (softmax_simt.cuh) where even those find an SM each and a
-    // row's keys are too few to be cut into parts instead
+    // on the FMA pipe (softmax_simt.cuh) where even those leave half of the SMs free
+    // (one kernel's blocks are placed while the last one's are there: twice as many
+    // share SMs and take twice as long) and a row's keys are too few to be cut into
+    // parts instead.  Backward with tiles of 16, 32, 64 rows, W = 64: 512 tokens of a
+    // head 39, 46, 72 us; 1024 of two 64, 46, 72; 2048 of two 65, 75, 74.
     const long long t64 = BH * ((p->Lq + 64 / pl->G - 1) / (64 / pl->G));
     const bool few = span <= 384;
-    pl->rpt = few && pl->G <= 16 && 4 * t64 <= sms ? 1 : few && pl->G <= 32 && 2 * t64 <= sms ? 2 : 4;
+    pl->rpt = few && pl->G <= 16 && 8 * t64 <= sms ? 1 : few && pl->G <= 32 && 4 * t64 <= sms ? 2 : 4;
     pl->nq = (pl->tc ? 128 : 16 * pl->rpt) / pl->G;
     const long long RT = (p->Lq + pl->nq - 1) / pl->nq;  // row tiles
     // The tensor-core forward's items are 4, 2 or 1 row tiles (see softmax_tc.cuh).
     // One leaves the fewest SMs idle where all tiles fit them at once; of many, two
-    // share the key chunks (long32k: 187 us, four 191, one 237), and four pay once
-    // a tile's band is long (8192 dense tokens: 430 us, two 454).
+    // share the key chunks (32768 tokens of 16 heads, W = 256: 187 us, four 191, one
+    // 237), and four pay once a tile's band is long (8192 dense tokens: 427 us, two 454).
     pl->nr = 1;
     if (pl->tc && BH * RT > sms) pl->nr = W >= 4096 && BH * RT >= 6LL * sms ? 4 : 2;
     pl->per = pl->nr * pl->nq;
@@ -69,7 +72,9 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     if (std::max(tiles, BH * pl->nktile) > (1LL << 30)) return SA_ERR_UNSUPPORTED;
     // A few query rows over many keys (single new tokens) would leave most SMs
     // idle: then every tile's keys are cut into parts for about two blocks an
-    // SM, of at least four chunks each, joined by a second kernel.
+    // SM, of at least four (bf16: eight) chunks each, joined by a second kernel.
+    // 64 query tokens of 8 heads over 32768: 32 us, not cut 199; 2048 dense fp32
+    // tokens of one head: 44 us, not cut 208.
     const long long keys = std::min<long long>(p->Lk, span + pl->per);
     const long long chunks = (keys + 63) / 64;
     pl->nsplit = 1;
@@ -79,8 +84,8 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     long long parts = pl->nparts > 1 ? pl->rows * pl->nparts : 0;
     // Few query rows per key head are bound by reading the keys and
     // values: a kernel without tiles, whose blocks (two per SM, of two chunks or
-    // more) share all sequences' chunks evenly, takes 48 us where the tiled forward
-    // takes 83 (8 sequences of 16384 to 32768 tokens, 4 heads to a key head, bf16).
+    // more) share all sequences' chunks evenly, takes 54 us where the tiled forward
+    // takes 85 (8 sequences of 32768 tokens, 4 key heads of 4 heads each, bf16).
     pl->token = 0;
     if ((long long)pl->G * p->Lq <= sm::token::max_rows(pl->tc) && p->B <= sm::token::MAXB && BH <= 4096 && BH > 0) {
         pl->token = (int)std::max<long long>(1, std::min<long long>(2LL * sms, BH * chunks / 2));
@@ -90,7 +95,8 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     const size_t head = kHeader + align_up((size_t)p->B * 8);
     pl->part_ml = head + align_up((size_t)parts * kD * 4);
     pl->fwd_bytes = pl->part_ml + align_up((size_t)parts * 8);
-    // the fp32 backward's tiles, where few, are cut likewise
+    // the fp32 backward's tiles, where few, are cut likewise (2048 dense tokens of
+    // one head: 122 us, not cut 596; the sums take two short kernels)
     const long long kchunks = (std::min<long long>(p->Lq, span + 64) + 63) / 64 * pl->G, kt = BH * pl->nktile;
     pl->qsplit = pl->ksplit = 1;
     if (!pl->tc && pl->rows > 0 && tiles < sms)
@@ -375,7 +381,8 @@ sa_status sinkhorn_attn_softmax_bwd(const sa_softmax_params* p, const void* q, c
     a.part_o = (float*)((char*)ws + pl.bwd_part);
     // With few keys a row's probabilities are large and dO . O, taken from the
     // rounded O, is off by about as much as the dS it is subtracted in: up to
-    // 64 keys the sweep forms D itself, in a pass of its own over them.
+    // 64 keys the sweep forms D itself, in a pass of its own over them (32768 tokens of 16
+    // heads, W = 16: 310 us, without 272).
     a.exact_d = p->dtype == SA_BF16 && (long long)a.W + a.R + 1 <= 64;
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = mask && pl.rows > 0 ? launch(sm::k_span, p->B, 1024, 0, st, a) : cudaSuccess;

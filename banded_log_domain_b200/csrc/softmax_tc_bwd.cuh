@@ -11,19 +11,22 @@
 // A unit is one row tile times one chunk.  Its S and G go to buffers of 64 columns
 // of TMEM, three pairs of them in DQ, a ring of five in DKV; their rows' operands
 // lie in TMEM too, copied there from shared memory at an item's start (an MMA with
-// its A operand in TMEM took 39-44 cycles at 64 columns, from shared memory 63-75).
-// A team of eight warps (two per lane quadrant, 32 columns each)
-// reads them, forms P and dS and writes them as bf16 over the S and G they came
-// from, from where the second products read them as their A operand.  Two teams
-// take the units in turn.  One warp issues S and G, another the second products
+// its A operand in TMEM took 39-44 cycles at 64 columns, from shared memory 63-75;
+// 8192 dense tokens of 16 heads: 1.29 -> 1.15 ms).  A team of eight warps (two per
+// lane quadrant, 32 columns each) reads them, forms P and dS and writes them as bf16
+// over the S and G they came from, from where the second products read them as their
+// A operand.  Two teams take the units in turn, and ask for their rows of the next
+// item while one ends (32768 tokens of 16 heads, W = 256: 0.54 -> 0.52 ms; there the
+// ends of the items, where the products drain, cost most, on dense problems the
+// exponentials and the hand-overs).  One warp issues S and G, another the second products
 // (one thread for all that add into an accumulator); a loader brings the tiles,
 // and an aux warp prepares each chunk's columns (mask words; zeroed operand rows
 // of tokens that are not in use, as 0 times what they hold need not be 0).  In DKV
 // u and D belong to columns: they enter S and G in the products themselves, as 16
 // more channels, u / c and -D in three bf16 parts each (2^-24 of them) against
-// ones; read by every thread from shared memory they cost the teams twice the
-// time, behind the products' own reads.  D = dO . O is formed by the teams' warps at an item's start, a
-// quarter of the channels each; one aux warp for all rows took 20 us an item.
+// ones (read by every thread from shared memory they cost the teams twice the
+// time, behind the products' own reads).  D = dO . O is formed by the teams' warps
+// at an item's start, a quarter of the channels each.
 #pragma once
 
 #include "softmax_tc.cuh"
@@ -70,7 +73,7 @@ struct Maps {
 
 // Byte offset of 16-byte piece c (0, 1) of row r in a tile of 32-byte rows, 32-byte swizzle.
 __device__ __forceinline__ uint32_t aug_off(int r, int c) { return r * 32 + ((c ^ ((r >> 2) & 1)) << 4); }
-// x as hi + mid + lo in bf16: the two words of slots 0-1 and 2-3 (3: next).
+// x as hi + mid + lo, the bits of three bf16 numbers.
 __device__ __forceinline__ void split3(float x, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
     const __nv_bfloat16 h = __float2bfloat16_rn(x);
     const float y = x - __bfloat162float(h);
