@@ -53,11 +53,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
-// 128 rows x 32 bytes (16 bf16 of K) of a K-major tile into 8 TMEM columns, one row
-// to a lane: an MMA's A operand.
-__device__ __forceinline__ void tmem_copy(uint32_t tmem, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
-}
 // Registers per thread of the calling warpgroup from here on.
 template <int N>
 __device__ __forceinline__ void reg_inc() {

@@ -8,17 +8,16 @@
 // with P = 2^(c2 S + u2).  (One sweep that also added into dQ would save two of
 // the seven products but needs atomics, whose order changes results.)
 //
-// A unit is one row tile times one chunk.  Its S and G go to buffers of 64 columns
-// of TMEM, three pairs of them in DQ, a ring of five in DKV; their rows' operands
-// lie in TMEM too, copied there from shared memory at an item's start (an MMA with
-// its A operand in TMEM took 39-44 cycles at 64 columns, from shared memory 63-75;
-// 8192 dense tokens of 16 heads: 1.29 -> 1.15 ms).  A team of eight warps (two per
-// lane quadrant, 32 columns each) reads them, forms P and dS and writes them as bf16
-// over the S and G they came from, from where the second products read them as their
-// A operand.  Two teams take the units in turn, and ask for their rows of the next
-// item while one ends (32768 tokens of 16 heads, W = 256: 0.54 -> 0.52 ms; there the
-// ends of the items, where the products drain, cost most, on dense problems the
-// exponentials and the hand-overs).  One warp issues S and G, another the second products
+// A unit is one row tile times one chunk.  S and G of a unit go to one of three
+// slots of TMEM; a team of eight warps (two per lane quadrant, 32 columns each)
+// reads them, forms P and dS and writes them as bf16 over the S and G they came
+// from, from where the second products read them as their A operand.  Two teams
+// take the units in turn, and ask for their rows of the next item while one ends
+// (32768 tokens of 16 heads, W = 256: 0.53 -> 0.51 ms).  (The row tiles' operands in TMEM as well made the MMAs shorter but left five
+// buffers of S or G in DKV and one accumulator in DQ: 3 % slower.)  A banded item
+// is bound by its start and its end, where the products drain; a long one by the
+// hand-overs (without any exponentials: 596 us for 643 at 8192 dense tokens of 8
+// heads).  One warp issues S and G, another the second products
 // (one thread for all that add into an accumulator); a loader brings the tiles,
 // and an aux warp prepares each chunk's columns (mask words; zeroed operand rows
 // of tokens that are not in use, as 0 times what they hold need not be 0).  In DKV
@@ -59,8 +58,8 @@ constexpr int OFF_ITEM = OFF_ONE + 2 * 4096;
 constexpr int OFF_XD = OFF_ITEM + NIT * (int)sizeof(Item);  // two buffers of shares of D, [4][128]
 constexpr int OFF_WORDS = OFF_XD + 4096;
 constexpr int OFF_BAR = OFF_WORDS + NST * 8;
-enum { RFULL = 0, REMPTY = 2, IFULL = 4, IEMPTY = IFULL + NIT, SGFULL = IEMPTY + NIT, DSFULL = SGFULL + NSLOT, SLOT = DSFULL + NSLOT, ACCFULL = SLOT + 6,
-       ACCEMPTY = ACCFULL + 1, ADONE = ACCEMPTY + 1, XDSUM = ADONE + 1, DRAIN = XDSUM + 1, FULL = DRAIN + 1, READY = FULL + NST,
+enum { RFULL = 0, REMPTY = 2, IFULL = 4, IEMPTY = IFULL + NIT, SGFULL = IEMPTY + NIT, DSFULL = SGFULL + NSLOT, SLOT = DSFULL + NSLOT, ACCFULL = SLOT + NSLOT,
+       ACCEMPTY = ACCFULL + 2, XDSUM = ACCEMPTY + 2, DRAIN = XDSUM + 1, FULL = DRAIN + 1, READY = FULL + NST,
        EMPTY = READY + NST, NBAR = EMPTY + NST };
 constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
 static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -128,17 +127,14 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
     float* xd = reinterpret_cast<float*>(sm + OFF_XD);
     Ctl ctl{bar, abort_flag, a.status};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // TMEM columns: the buffers of S and G from 0, accumulators to 447, then the
-    // row tile's operands, 32 columns each
-    constexpr int ACC = MODE == DQ ? 384 : 320, ROWS = 448, NBUF = MODE == DQ ? 6 : 5;
-    // The columns and barriers of a unit's S (z = 0) and G (z = 1): the buffers in turn.
-    auto buf = [](int gu, int z) { return (2 * gu + z) % NBUF; };
-    auto uses = [](int gu, int z) { return (2 * gu + z) / NBUF; };  // of that buffer before
+    constexpr int NACC = MODE == DQ ? 2 : 1;  // accumulator buffers (DQ: of 64 columns; DKV: of 128)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar + RFULL + i, 1);
             tc::mbar_init(bar + REMPTY + i, MODE == DQ ? 17 : 1);  // the MMAs, and the warps that read dO
+            tc::mbar_init(bar + ACCFULL + i, 1);
+            tc::mbar_init(bar + ACCEMPTY + i, 16);
         }
         for (int i = 0; i < NIT; ++i) {
             tc::mbar_init(bar + IFULL + i, 1);
@@ -147,16 +143,13 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
         for (int i = 0; i < NSLOT; ++i) {
             tc::mbar_init(bar + SGFULL + i, 1);
             tc::mbar_init(bar + DSFULL + i, 8);
+            tc::mbar_init(bar + SLOT + i, 1);
         }
         for (int s = 0; s < NST; ++s) {
             tc::mbar_init(bar + FULL + s, 1);
             tc::mbar_init(bar + READY + s, 1);
             tc::mbar_init(bar + EMPTY + s, 1);
         }
-        for (int i = 0; i < 6; ++i) tc::mbar_init(bar + SLOT + i, 1);
-        tc::mbar_init(bar + ACCFULL, 1);
-        tc::mbar_init(bar + ACCEMPTY, 16);
-        tc::mbar_init(bar + ADONE, 1);
         tc::mbar_init(bar + XDSUM, 16);
         tc::mbar_init(bar + DRAIN, 2);
         *abort_flag = 0;
@@ -178,7 +171,8 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tm = *tbase, tA = tm + ACC, tR = tm + ROWS;
+    // TMEM columns: slot x: S at 128 x, G at 128 x + 64; accumulators from 384
+    const uint32_t tm = *tbase, tA = tm + 384;
     tc::grid_dep_wait();
     tc::grid_dep_launch();
     if (MODE == DQ && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
@@ -301,49 +295,34 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             for (int it = 0; ok && begin_item(it); ++it) {
                 const int rb = it & 1, nu = items[it % NIT].n * passes;
                 if (!ctl.wait_warp(RFULL + rb, (it >> 1) & 1)) break;
-                // the rows' operands into TMEM, once the products of the item before have read theirs
-                if (it > 0 && !ctl.wait_warp(ADONE, (it - 1) & 1)) break;
-                tc::tc_fence_after();
-                if (tc::elect_one()) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        tmem_copy(tR + 8 * k, tc::sdesc_add(dR, (2 * rb + (k >> 2)) * TILE + 32 * (k & 3)));
-                }
-                __syncwarp();
+                const uint64_t dA = tc::sdesc_add(dR, 2 * rb * TILE);
                 for (int u = 0; u < nu; ++u, ++gu) {
                     const int s = gu % NST, x = gu % NSLOT;
-                    if (!ctl.wait_warp(READY + s, (gu / NST) & 1)) {
+                    if (!ctl.wait_warp(READY + s, (gu / NST) & 1) ||
+                        (gu >= NSLOT && !ctl.wait_warp(SLOT + x, ((gu / NSLOT) - 1) & 1))) {
                         ok = false;
                         break;
                     }
+                    tc::tc_fence_after();
                     const uint64_t dB = tc::sdesc_add(dC, s * 2 * KT);
+                    if (tc::elect_one()) {
 #pragma unroll
-                    for (int z = 0; z < 2; ++z) {  // S, G
-                        const int i = buf(gu, z), n = uses(gu, z);
-                        if (n > 0 && !ctl.wait_warp(SLOT + i, (n - 1) & 1)) {
-                            ok = false;
-                            break;
-                        }
-                        tc::tc_fence_after();
-                        if (tc::elect_one()) {
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma_bf16(tm + 128 * x, tc::sdesc_add(dA, 32 * k), tc::sdesc_add(dB, 32 * k), id, k > 0);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                tc::mma_bf16_ts(tm + 64 * i, tR + 32 * z + 8 * k, tc::sdesc_add(dB, z * KT + 32 * k), id,
-                                                k > 0);
-                            if (MODE == DKV)  // S + u / c, G - D
-                                tc::mma_bf16(tm + 64 * i, tc::sdesc_add(dOne, z * 4096), tc::sdesc_add(dAug, s * AUG), id,
-                                             1u);
-                            if (z == 1) tc::tc_commit(bar + SGFULL + x);
+                        for (int k = 0; k < 4; ++k)
+                            tc::mma_bf16(tm + 128 * x + 64, tc::sdesc_add(dA, TILE + 32 * k),
+                                         tc::sdesc_add(dB, KT + 32 * k), id, k > 0);
+                        if (MODE == DKV) {  // S + u / c, G - D
+                            tc::mma_bf16(tm + 128 * x, dOne, tc::sdesc_add(dAug, s * AUG), id, 1u);
+                            tc::mma_bf16(tm + 128 * x + 64, tc::sdesc_add(dOne, 4096), tc::sdesc_add(dAug, s * AUG), id, 1u);
                         }
-                        __syncwarp();
+                        tc::tc_commit(bar + SGFULL + x);
                     }
-                    if (!ok) break;
+                    __syncwarp();
                 }
                 if (!ok) break;
-                if (tc::elect_one()) {
-                    tc::tc_commit(bar + REMPTY + rb);
-                    tc::tc_commit(bar + ADONE);
-                }
+                if (tc::elect_one()) tc::tc_commit(bar + REMPTY + rb);
                 end_item(it);
             }
             if (tc::elect_one()) tc::tc_commit(bar + DRAIN);
@@ -358,41 +337,40 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             for (int it = 0; ok && begin_item(it); ++it) {
                 const int n = items[it % NIT].n, nu = n * passes;
                 const int skip = EXACT ? n : 0;  // units of the pass that only sums
+                const int ab = na % NACC;
                 for (int u = 0; u < nu; ++u, ++gu) {
-                    const int s = gu % NST, x = gu % NSLOT, i0 = buf(gu, 0), i1 = buf(gu, 1);
-                    if ((u == skip && na > 0 && !ctl.wait_warp(ACCEMPTY, (na - 1) & 1)) ||
+                    const int s = gu % NST, x = gu % NSLOT;
+                    if ((u == skip && na >= NACC && !ctl.wait_warp(ACCEMPTY + ab, ((na / NACC) - 1) & 1)) ||
                         !ctl.wait_warp(DSFULL + x, (gu / NSLOT) & 1)) {
                         ok = false;
                         break;
                     }
                     tc::tc_fence_after();
                     const uint64_t dB = tc::sdesc_add(dC, s * 2 * KT);
-                    const uint32_t b0 = tm + 64 * i0, b1 = tm + 64 * i1;
+                    const uint32_t slot = tm + 128 * x, acc = tA + (MODE == DQ ? 64 * ab : 0);
                     if (tc::elect_one()) {
-                        // 16 columns of the chunk are 8 of TMEM; each half of a
-                        // buffer keeps the columns it was formed from
-                        if (MODE == DQ) {
-                            if (u >= skip) {
+                        if (u >= skip) {
+                            // 16 columns of the chunk are 8 of TMEM; each half of a
+                            // slot's S (or G) keeps the columns it was formed from
+                            if (MODE == DQ) {
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
-                                    tc::mma_bf16_ts(tA, b0 + 32 * (k >> 1) + 8 * (k & 1), tc::sdesc_add(dB, k * 2048), id,
+                                    tc::mma_bf16_ts(acc, slot + 32 * (k >> 1) + 8 * (k & 1), tc::sdesc_add(dB, k * 2048), id,
                                                     (u > skip || k > 0) ? 1u : 0u);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    tc::mma_bf16_ts(acc, slot + 32 * (k >> 1) + 8 * (k & 1),
+                                                    tc::sdesc_add(dB, KT + k * 2048), id, (u > 0 || k > 0) ? 1u : 0u);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    tc::mma_bf16_ts(acc + 64, slot + 64 + 32 * (k >> 1) + 8 * (k & 1),
+                                                    tc::sdesc_add(dB, k * 2048), id, (u > 0 || k > 0) ? 1u : 0u);
                             }
-                            tc::tc_commit(bar + SLOT + i0);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                tc::mma_bf16_ts(tA, b0 + 32 * (k >> 1) + 8 * (k & 1), tc::sdesc_add(dB, KT + k * 2048), id,
-                                                (u > 0 || k > 0) ? 1u : 0u);
-                            tc::tc_commit(bar + SLOT + i0);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                tc::mma_bf16_ts(tA + 64, b1 + 32 * (k >> 1) + 8 * (k & 1), tc::sdesc_add(dB, k * 2048), id,
-                                                (u > 0 || k > 0) ? 1u : 0u);
                         }
-                        tc::tc_commit(bar + SLOT + i1);
+                        tc::tc_commit(bar + SLOT + x);
                         tc::tc_commit(bar + EMPTY + s);
-                        if (u == nu - 1) tc::tc_commit(bar + ACCFULL);
+                        if (u == nu - 1) tc::tc_commit(bar + ACCFULL + ab);
                     }
                     __syncwarp();
                 }
@@ -511,8 +489,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                     break;
                 }
                 tc::tc_fence_after();
-                const uint32_t mS = tm + 64 * buf(gv0, 0) + lanebase + 32 * hf;
-                const uint32_t mG = tm + 64 * buf(gv0, 1) + lanebase + 32 * hf;
+                const uint32_t mS = tm + 128 * x + lanebase + 32 * hf, mG = mS + 64;
                 const int j0 = 64 * c + 32 * hf;
                 uint32_t on = a.mask ? words[2 * s + hf] : ~0u;
                 const bool full = j0 >= wlo && j0 + 31 <= whi && on == ~0u;
@@ -588,8 +565,9 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             }
             if (MODE == DQ && begin_item(it + 1)) ask(items[(it + 1) % NIT]);
             // the accumulators: this warp's lanes, 16 columns
+            const int ab = na % NACC;
             if (nu > 0) {
-                if (!ctl.wait_warp(ACCFULL, na & 1)) break;
+                if (!ctl.wait_warp(ACCFULL + ab, (na / NACC) & 1)) break;
                 ++na;
                 tc::tc_fence_after();
             }
@@ -597,7 +575,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             for (int k = 0; k < (MODE == DQ ? 1 : 2); ++k) {
                 uint32_t o[16];
                 if (nu > 0) {
-                    tc::tmem_ld16(tA + 64 * k + lanebase + 16 * q4, o);
+                    tc::tmem_ld16(tA + (MODE == DQ ? 64 * ab : 64 * k) + lanebase + 16 * q4, o);
                     tc::tmem_wait_ld();
                 }
                 const float f = MODE == DKV && k == 0 ? 1.f : a.c;
@@ -623,7 +601,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             if (nu > 0) {
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bar + ACCEMPTY);
+                if (lane == 0) tc::mbar_arrive(bar + ACCEMPTY + ab);
             }
             end_item(it);
         }
