@@ -12,12 +12,15 @@
 // slots of TMEM; a team of eight warps (two per lane quadrant, 32 columns each)
 // reads them, forms P and dS and writes them as bf16 over the S and G they came
 // from, from where the second products read them as their A operand.  Two teams
-// take the units in turn, and ask for their rows of the next item while one ends
-// (32768 tokens of 16 heads, W = 256: 0.53 -> 0.51 ms).  (The row tiles' operands in TMEM as well made the MMAs shorter but left five
-// buffers of S or G in DKV and one accumulator in DQ: 3 % slower.)  A banded item
-// is bound by its start and its end, where the products drain; a long one by the
-// hand-overs (without any exponentials: 596 us for 643 at 8192 dense tokens of 8
-// heads).  One warp issues S and G, another the second products
+// take the units in turn; in DQ they ask for their rows of the next item while one
+// ends (32768 tokens of 16 heads, W = 256: 0.53 -> 0.51 ms for both sweeps), in DKV
+// one writes an item's gradients while the other begins the next (0.51 -> 0.49 ms;
+// DQ's teams form D together, and apart took longer).  (The row tiles' operands in
+// TMEM as well made the MMAs shorter but left five buffers of S or G in DKV and one
+// accumulator in DQ: 3 % slower.)  A banded item is bound by its start and its end,
+// where the products drain; a long one by the hand-overs (without any exponentials
+// 8192 dense tokens of 8 heads took 596 us for 643).  One warp issues S and G,
+// another the second products
 // (one thread for all that add into an accumulator); a loader brings the tiles,
 // and an aux warp prepares each chunk's columns (mask words; zeroed operand rows
 // of tokens that are not in use, as 0 times what they hold need not be 0).  In DKV
@@ -134,7 +137,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             tc::mbar_init(bar + RFULL + i, 1);
             tc::mbar_init(bar + REMPTY + i, MODE == DQ ? 17 : 1);  // the MMAs, and the warps that read dO
             tc::mbar_init(bar + ACCFULL + i, 1);
-            tc::mbar_init(bar + ACCEMPTY + i, 16);
+            tc::mbar_init(bar + ACCEMPTY + i, MODE == DQ ? 16 : 8);
         }
         for (int i = 0; i < NIT; ++i) {
             tc::mbar_init(bar + IFULL + i, 1);
@@ -370,7 +373,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                         }
                         tc::tc_commit(bar + SLOT + x);
                         tc::tc_commit(bar + EMPTY + s);
-                        if (u == nu - 1) tc::tc_commit(bar + ACCFULL + ab);
+                        if (u == nu - 1) tc::tc_commit(bar + ACCFULL + (MODE == DQ ? ab : gu & 1));
                     }
                     __syncwarp();
                 }
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
         const uint32_t lanebase = (uint32_t)(qd * 32) << 16;
         const uint64_t c2p = tc::pk2(a.c2, a.c2);
         const float uscale = 1.f / a.c;
-        int gu = 0, na = 0, nx = 0;
+        int gu = 0, na = 0, nx = 0;  // units, items whose accumulators this team read, sums of D
         bool ok = true;
         // The sum over the four warps that hold a row's columns.  Two buffers: to
         // reach the one after the next, every warp has read this one.
@@ -564,44 +567,47 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                 a.aug[2 * at + 1] = make_uint4(0u, 0u, 0u, 0u);
             }
             if (MODE == DQ && begin_item(it + 1)) ask(items[(it + 1) % NIT]);
-            // the accumulators: this warp's lanes, 16 columns
+            // The accumulators, this warp's lanes.  DQ: 16 columns.  DKV: 32 of each,
+            // by the team that had the last unit; the other is at the next item.
             const int ab = na % NACC;
-            if (nu > 0) {
-                if (!ctl.wait_warp(ACCFULL + ab, (na / NACC) & 1)) break;
+            const bool mine = MODE == DQ || (((nu > 0 ? gu - 1 : 0) ^ team) & 1) == 0;
+            if (nu > 0 && mine) {  // ACCFULL: one per buffer (DQ), per team (DKV)
+                if (!ctl.wait_warp(ACCFULL + (MODE == DQ ? ab : team), (na / NACC) & 1)) break;
                 ++na;
                 tc::tc_fence_after();
             }
+            if (mine) {
 #pragma unroll
-            for (int k = 0; k < (MODE == DQ ? 1 : 2); ++k) {
-                uint32_t o[16];
-                if (nu > 0) {
-                    tc::tmem_ld16(tA + (MODE == DQ ? 64 * ab : 64 * k) + lanebase + 16 * q4, o);
-                    tc::tmem_wait_ld();
-                }
-                const float f = MODE == DKV && k == 0 ? 1.f : a.c;
-                __nv_bfloat16* out = nullptr;
-                if (exists)
-                    out = MODE == DQ ? a.dq.at<__nv_bfloat16>(w.b, w.hk * a.G + g, i)
-                                     : (k == 0 ? a.dv : a.dk).at<__nv_bfloat16>(w.b, w.hk, i);
-                if (out) {
-                    uint4* p = reinterpret_cast<uint4*>(out + 16 * q4);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t y[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            y[e] = nu > 0 ? tc::pack_bf16(__uint_as_float(o[8 * j + 2 * e]) * f,
-                                                          __uint_as_float(o[8 * j + 2 * e + 1]) * f)
-                                          : 0u;
-                        p[j] = make_uint4(y[0], y[1], y[2], y[3]);
+                for (int k = 0; k < (MODE == DQ ? 1 : 4); ++k) {
+                    const int col = MODE == DQ ? 16 * q4 : 32 * hf + 16 * (k & 1);
+                    uint32_t o[16];
+                    if (nu > 0) {
+                        tc::tmem_ld16(tA + 64 * (MODE == DQ ? ab : k >> 1) + lanebase + col, o);
+                        tc::tmem_wait_ld();
                     }
+                    const float f = MODE == DKV && k < 2 ? 1.f : a.c;
+                    if (exists) {
+                        uint4* p = reinterpret_cast<uint4*>(
+                            (MODE == DQ ? a.dq.at<__nv_bfloat16>(w.b, w.hk * a.G + g, i)
+                                        : (k < 2 ? a.dv : a.dk).at<__nv_bfloat16>(w.b, w.hk, i)) + col);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                y[e] = nu > 0 ? tc::pack_bf16(__uint_as_float(o[8 * j + 2 * e]) * f,
+                                                              __uint_as_float(o[8 * j + 2 * e + 1]) * f)
+                                              : 0u;
+                            p[j] = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-            }
-            if (nu > 0) {
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bar + ACCEMPTY + ab);
+                if (nu > 0) {
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(bar + ACCEMPTY + ab);
+                }
             }
             end_item(it);
         }
