@@ -39,7 +39,6 @@ struct Args {
     float* part_o;        // [row][part][64], then
     float2* part_ml;      // [row][part]: running maximum (log2 units) and sum
     int nparts;
-    int exact_d;          // dQ sweep: D from a first pass over the keys
 
     // position of query 0 of sequence b
     __device__ __forceinline__ long long first(int b) const { return q_pos ? q_pos[b] : Lk - Lq; }

@@ -39,6 +39,8 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     if (p->Lq > p->Lk) return SA_ERR_INVALID_ARG;
     if (p->Hk == 0 ? p->Hq != 0 : p->Hq % p->Hk != 0) return SA_ERR_INVALID_ARG;
     if (p->d != kD) return SA_ERR_UNSUPPORTED;
+    // u / c and 1 / c stay far from fp32's ends (the backward forms both)
+    if (p->eps < 0x1p-100f || p->eps > 0x1p100f) return SA_ERR_UNSUPPORTED;
     pl->G = p->Hk ? std::max(1, p->Hq / p->Hk) : 1;
     if (pl->G > kMaxGroup) return SA_ERR_UNSUPPORTED;
     // token indices stay clear of 2^31 with a tile's rows added
@@ -161,7 +163,6 @@ void base_args(sm::Args* a, const sa_softmax_params* p, const Plan& pl, const ui
     a->ntile = pl.ntile;
     a->nsplit = 1;
     a->nparts = 1;
-    a->exact_d = 0;
 }
 
 cudaError_t fwd_f32(const sa_softmax_params* p, const Plan& pl, const sm::Args& a, cudaStream_t st) {
@@ -297,13 +298,13 @@ cudaError_t zero_grads(const sa_softmax_params* p, sm::Args& a, cudaStream_t st)
     return launch(sm::k_zero<__nv_bfloat16>, (n + 3) / 4, 128, 0, st, a);
 }
 
-cudaError_t bwd_launch(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cudaStream_t st) {
+cudaError_t bwd_launch(const sa_softmax_params* p, const Plan& pl, sm::Args& a, bool exact_d, cudaStream_t st) {
     if (!pl.tc) return bwd_f32(p, pl, a, st);
     const long long BH = (long long)p->B * p->Hk;
     a.nq = pl.nq;
     a.ntile = (p->Lq + a.nq - 1) / a.nq;
-    const cudaError_t e = a.exact_d ? bwd_tc<sm::tcf::bwd::DQ, true>(p, a, BH * a.ntile, st)
-                                    : bwd_tc<sm::tcf::bwd::DQ, false>(p, a, BH * a.ntile, st);
+    const cudaError_t e = exact_d ? bwd_tc<sm::tcf::bwd::DQ, true>(p, a, BH * a.ntile, st)
+                                  : bwd_tc<sm::tcf::bwd::DQ, false>(p, a, BH * a.ntile, st);
     return e != cudaSuccess ? e : bwd_tc<sm::tcf::bwd::DKV, false>(p, a, BH * ((p->Lk + 127) / 128), st);
 }
 
@@ -379,14 +380,14 @@ sa_status sinkhorn_attn_softmax_bwd(const sa_softmax_params* p, const void* q, c
     a.D = (float*)((char*)ws + kHeader + align_up((size_t)p->B * 8));
     a.aug = (uint4*)a.D;
     a.part_o = (float*)((char*)ws + pl.bwd_part);
-    // With few keys a row's probabilities are large and dO . O, taken from the
+    // bf16: with few keys a row's probabilities are large and dO . O, taken from the
     // rounded O, is off by about as much as the dS it is subtracted in: up to
     // 64 keys the sweep forms D itself, in a pass of its own over them (32768 tokens of 16
     // heads, W = 16: 310 us, without 272).
-    a.exact_d = p->dtype == SA_BF16 && (long long)a.W + a.R + 1 <= 64;
+    const bool exact_d = (long long)a.W + a.R + 1 <= 64;
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = mask && pl.rows > 0 ? launch(sm::k_span, p->B, 1024, 0, st, a) : cudaSuccess;
-    if (e == cudaSuccess) e = pl.rows > 0 ? bwd_launch(p, pl, a, st) : zero_grads(p, a, st);
+    if (e == cudaSuccess) e = pl.rows > 0 ? bwd_launch(p, pl, a, exact_d, st) : zero_grads(p, a, st);
     return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 

@@ -400,7 +400,7 @@ typedef struct {
     int B, Hq, Hk, Lq, Lk, d;  /* d == 64, Hq a multiple of Hk, Hq / Hk <= 64,
                                   B Hq <= 65535, Lq <= Lk <= 2^30 */
     int W;                     /* band half-width, W >= 0 (W >= Lk - 1 is dense) */
-    float eps;                 /* temperature, > 0 */
+    float eps;                 /* temperature, 2^-100 .. 2^100 */
     int causal;                /* 0 or 1: keys at later positions are left out */
     sa_dtype dtype;            /* element type of Q, K, V, O, dO, dQ, dK, dV */
     long long q_stride[3], k_stride[3], v_stride[3], o_stride[3];

@@ -32,6 +32,14 @@ def test_bad_sizes_are_refused(kw, status):
     assert lib.sinkhorn_attn_softmax_bwd(ctypes.byref(p), *[None] * 12, 1 << 40, None) == status
 
 
+@pytest.mark.parametrize("eps,status", [(2.0 ** -100, 0), (2.0 ** 100, 0), (2.0 ** -101, -2), (2.0 ** 101, -2),
+                                        (1e-45, -2), (3.4e38, -2)])
+def test_temperatures_at_the_ends_of_fp32_are_refused(eps, status):
+    lib = sa.load()
+    for dt in (sa.SA_F32, sa.SA_BF16):
+        assert lib.sinkhorn_attn_softmax_workspace_size(ctypes.byref(P(eps=eps, dtype=dt)), None, None) == status
+
+
 def test_null_params_small_workspace_and_host_pointers():
     lib = sa.load()
     assert lib.sinkhorn_attn_softmax_fwd(None, *[None] * 8, 1 << 40, None) == -1

@@ -80,6 +80,30 @@ def test_masks(dtype, kind, W):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("L", [60, 130])
+@pytest.mark.parametrize("W", [3, 130])
+def test_masks_of_small_problems(dtype, L, W):
+    # fp32 tiles of 16 and of 32 rows
+    q, k, v, dO = draw(dtype, 3, 4, 2, L, L, seed=L)
+    mask = (torch.rand(3, L, generator=torch.Generator("cuda").manual_seed(W), device="cuda") < 0.5).to(torch.uint8)
+    mask[2] = 0
+    off = (mask == 0)[:, None, :, None]
+    for i, t in enumerate((q, k, v, dO)):
+        t.masked_fill_(off, (float("nan"), float("inf"))[i % 2])
+    for causal in (False, True):
+        check(q, k, v, dO, W=W, mask=mask, causal=causal)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("eps", [2.0 ** -20, 2.0 ** 30, 2.0 ** 100])
+def test_temperatures_far_from_one(dtype, eps):
+    # q grows with eps, so that the scores stay; at 2^100 it cannot, and they vanish
+    q, k, v, dO = draw(dtype, 1, 2, 2, 150, 150, seed=3)
+    f = eps if eps < 2.0 ** 40 else 1.0
+    check(q * f, k, v, dO, W=70, eps=eps)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("G", [1, 4, 7])
 @pytest.mark.parametrize("Lq,Lk,W", [(1, 1, 0), (1, 70, 70), (1, 1000, 1000), (1, 5000, 5000), (1, 5000, 300),
                                      (2, 130, 130), (5, 4096, 4096), (17, 3001, 3001), (40, 3001, 900)])
