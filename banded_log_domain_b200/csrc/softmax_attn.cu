@@ -271,7 +271,7 @@ bool make_map_aug(CUtensorMap* m, void* p, int L, int BH) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, bool EXACT>
+template <int MODE>
 cudaError_t bwd_tc(const sa_softmax_params* p, const sm::Args& a, long long items, cudaStream_t st) {
     using namespace sm::tcf::bwd;
     Maps maps;
@@ -286,8 +286,8 @@ cudaError_t bwd_tc(const sa_softmax_params* p, const sm::Args& a, long long item
              make_map_aug(&maps.X, a.aug, p->Lq, p->B * p->Hq);
     if (!ok) return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)std::min<long long>(items, sm_count());
-    cudaError_t e = cudaFuncSetAttribute(tc_bwd<MODE, EXACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    if (e == cudaSuccess) e = launch_pdl(tc_bwd<MODE, EXACT>, dim3(grid), dim3(THREADS), SMEM, st, a, maps, (int)items);
+    cudaError_t e = cudaFuncSetAttribute(tc_bwd<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e == cudaSuccess) e = launch_pdl(tc_bwd<MODE>, dim3(grid), dim3(THREADS), SMEM, st, a, maps, (int)items);
     return e;
 }
 
@@ -298,14 +298,13 @@ cudaError_t zero_grads(const sa_softmax_params* p, sm::Args& a, cudaStream_t st)
     return launch(sm::k_zero<__nv_bfloat16>, (n + 3) / 4, 128, 0, st, a);
 }
 
-cudaError_t bwd_launch(const sa_softmax_params* p, const Plan& pl, sm::Args& a, bool exact_d, cudaStream_t st) {
+cudaError_t bwd_launch(const sa_softmax_params* p, const Plan& pl, sm::Args& a, cudaStream_t st) {
     if (!pl.tc) return bwd_f32(p, pl, a, st);
     const long long BH = (long long)p->B * p->Hk;
     a.nq = pl.nq;
     a.ntile = (p->Lq + a.nq - 1) / a.nq;
-    const cudaError_t e = exact_d ? bwd_tc<sm::tcf::bwd::DQ, true>(p, a, BH * a.ntile, st)
-                                  : bwd_tc<sm::tcf::bwd::DQ, false>(p, a, BH * a.ntile, st);
-    return e != cudaSuccess ? e : bwd_tc<sm::tcf::bwd::DKV, false>(p, a, BH * ((p->Lk + 127) / 128), st);
+    const cudaError_t e = bwd_tc<sm::tcf::bwd::DQ>(p, a, BH * a.ntile, st);
+    return e != cudaSuccess ? e : bwd_tc<sm::tcf::bwd::DKV>(p, a, BH * ((p->Lk + 127) / 128), st);
 }
 
 }  // namespace
@@ -380,14 +379,9 @@ sa_status sinkhorn_attn_softmax_bwd(const sa_softmax_params* p, const void* q, c
     a.D = (float*)((char*)ws + kHeader + align_up((size_t)p->B * 8));
     a.aug = (uint4*)a.D;
     a.part_o = (float*)((char*)ws + pl.bwd_part);
-    // bf16: with few keys a row's probabilities are large and dO . O, taken from the
-    // rounded O, is off by about as much as the dS it is subtracted in: up to
-    // 64 keys the sweep forms D itself, in a pass of its own over them (32768 tokens of 16
-    // heads, W = 16: 310 us, without 272).
-    const bool exact_d = (long long)a.W + a.R + 1 <= 64;
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = mask && pl.rows > 0 ? launch(sm::k_span, p->B, 1024, 0, st, a) : cudaSuccess;
-    if (e == cudaSuccess) e = pl.rows > 0 ? bwd_launch(p, pl, a, exact_d, st) : zero_grads(p, a, st);
+    if (e == cudaSuccess) e = pl.rows > 0 ? bwd_launch(p, pl, a, st) : zero_grads(p, a, st);
     return e == cudaSuccess ? SA_OK : SA_ERR_CUDA;
 }
 

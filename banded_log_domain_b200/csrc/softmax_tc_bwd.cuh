@@ -2,11 +2,16 @@
 //
 // Two sweeps, so that every gradient is summed in one place and in one order:
 //   DQ    rows: 128 packed query rows;  chunks: 64 keys
-//         S = Q K^T, G = dO V^T, dS = P (G - D),  dQ += dS K
+//         S = Q K^T, G = dO V^T, dS = P (G - D),  dQ += dS K, X += P K
 //   DKV   rows: 128 keys;  chunks: 64 queries of one head after another
 //         S^T = K Q^T, G^T = V dO^T,  dV += P^T dO,  dK += dS^T Q
 // with P = 2^(c2 S + u2).  (One sweep that also added into dQ would save two of
-// the seven products but needs atomics, whose order changes results.)
+// the products but needs atomics, whose order changes results.)
+//
+// D = dO . O from the rounded O lacks r, |r| up to 2^-8 |D|: where few keys hold a
+// row's weight as much as the dS it is subtracted in.  As the rows of P sum to 1,
+// r is the sum of dS; it is summed in DQ beside the products, dQ is set right by
+// r X at the item's end, and DKV takes D + r.
 //
 // A unit is one row tile times one chunk.  S and G of a unit go to one of three
 // slots of TMEM; a team of eight warps (two per lane quadrant, 32 columns each)
@@ -62,7 +67,7 @@ constexpr int OFF_XD = OFF_ITEM + NIT * (int)sizeof(Item);  // two buffers of sh
 constexpr int OFF_WORDS = OFF_XD + 4096;
 constexpr int OFF_BAR = OFF_WORDS + NST * 8;
 enum { RFULL = 0, REMPTY = 2, IFULL = 4, IEMPTY = IFULL + NIT, SGFULL = IEMPTY + NIT, DSFULL = SGFULL + NSLOT, SLOT = DSFULL + NSLOT, ACCFULL = SLOT + NSLOT,
-       ACCEMPTY = ACCFULL + 2, XDSUM = ACCEMPTY + 2, DRAIN = XDSUM + 1, FULL = DRAIN + 1, READY = FULL + NST,
+       ACCEMPTY = ACCFULL + 2, XDSUM = ACCEMPTY + 1, DRAIN = XDSUM + 1, FULL = DRAIN + 1, READY = FULL + NST,
        EMPTY = READY + NST, NBAR = EMPTY + NST };
 constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
 static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -117,8 +122,7 @@ __device__ __forceinline__ void make_item(const Args& a, int idx, Item& w) {
     w.n = (hi - lo + 64) / 64;  // 0 when empty
 }
 
-// EXACT (DQ): D is summed in a first pass over the chunks.
-template <int MODE, bool EXACT>
+template <int MODE>
 __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_constant__ Maps maps, int nitems) {
     extern __shared__ uint8_t smraw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smraw + 1023) & ~(uintptr_t)1023);
@@ -130,14 +134,12 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
     float* xd = reinterpret_cast<float*>(sm + OFF_XD);
     Ctl ctl{bar, abort_flag, a.status};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int NACC = MODE == DQ ? 2 : 1;  // accumulator buffers (DQ: of 64 columns; DKV: of 128)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar + RFULL + i, 1);
             tc::mbar_init(bar + REMPTY + i, MODE == DQ ? 17 : 1);  // the MMAs, and the warps that read dO
             tc::mbar_init(bar + ACCFULL + i, 1);
-            tc::mbar_init(bar + ACCEMPTY + i, MODE == DQ ? 16 : 8);
         }
         for (int i = 0; i < NIT; ++i) {
             tc::mbar_init(bar + IFULL + i, 1);
@@ -153,6 +155,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             tc::mbar_init(bar + READY + s, 1);
             tc::mbar_init(bar + EMPTY + s, 1);
         }
+        tc::mbar_init(bar + ACCEMPTY, MODE == DQ ? 16 : 8);
         tc::mbar_init(bar + XDSUM, 16);
         tc::mbar_init(bar + DRAIN, 2);
         *abort_flag = 0;
@@ -187,9 +190,8 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar + IEMPTY + it % NIT);
     };
-    // units of an item: its chunks, for each head of the group (DKV), or twice
-    // (EXACT: first D = sum_j P G, then the gradient)
-    const int passes = MODE == DKV ? a.G : EXACT ? 2 : 1;
+    // units of an item: its chunks, for each head of the group in DKV
+    const int passes = MODE == DKV ? a.G : 1;
 
     if (warp >= 16) {
         reg_dec<REG_OTHER>();
@@ -338,42 +340,32 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             int gu = 0, na = 0;  // units, items with any
             bool ok = true;
             for (int it = 0; ok && begin_item(it); ++it) {
-                const int n = items[it % NIT].n, nu = n * passes;
-                const int skip = EXACT ? n : 0;  // units of the pass that only sums
-                const int ab = na % NACC;
+                const int nu = items[it % NIT].n * passes;
                 for (int u = 0; u < nu; ++u, ++gu) {
                     const int s = gu % NST, x = gu % NSLOT;
-                    if ((u == skip && na >= NACC && !ctl.wait_warp(ACCEMPTY + ab, ((na / NACC) - 1) & 1)) ||
+                    if ((u == 0 && na > 0 && !ctl.wait_warp(ACCEMPTY, (na - 1) & 1)) ||
                         !ctl.wait_warp(DSFULL + x, (gu / NSLOT) & 1)) {
                         ok = false;
                         break;
                     }
                     tc::tc_fence_after();
                     const uint64_t dB = tc::sdesc_add(dC, s * 2 * KT);
-                    const uint32_t slot = tm + 128 * x, acc = tA + (MODE == DQ ? 64 * ab : 0);
+                    const uint32_t slot = tm + 128 * x;
                     if (tc::elect_one()) {
-                        if (u >= skip) {
-                            // 16 columns of the chunk are 8 of TMEM; each half of a
-                            // slot's S (or G) keeps the columns it was formed from
-                            if (MODE == DQ) {
+                        // 16 columns of the chunk are 8 of TMEM; each half of a
+                        // slot's S (or G) keeps the columns it was formed from
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    tc::mma_bf16_ts(acc, slot + 32 * (k >> 1) + 8 * (k & 1), tc::sdesc_add(dB, k * 2048), id,
-                                                    (u > skip || k > 0) ? 1u : 0u);
-                            } else {
+                        for (int k = 0; k < 4; ++k)  // P times K, dO
+                            tc::mma_bf16_ts(tA, slot + 32 * (k >> 1) + 8 * (k & 1),
+                                            tc::sdesc_add(dB, (MODE == DQ ? 0 : KT) + k * 2048), id,
+                                            (u > 0 || k > 0) ? 1u : 0u);
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    tc::mma_bf16_ts(acc, slot + 32 * (k >> 1) + 8 * (k & 1),
-                                                    tc::sdesc_add(dB, KT + k * 2048), id, (u > 0 || k > 0) ? 1u : 0u);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    tc::mma_bf16_ts(acc + 64, slot + 64 + 32 * (k >> 1) + 8 * (k & 1),
-                                                    tc::sdesc_add(dB, k * 2048), id, (u > 0 || k > 0) ? 1u : 0u);
-                            }
-                        }
+                        for (int k = 0; k < 4; ++k)  // dS times K, Q
+                            tc::mma_bf16_ts(tA + 64, slot + 64 + 32 * (k >> 1) + 8 * (k & 1),
+                                            tc::sdesc_add(dB, k * 2048), id, (u > 0 || k > 0) ? 1u : 0u);
                         tc::tc_commit(bar + SLOT + x);
                         tc::tc_commit(bar + EMPTY + s);
-                        if (u == nu - 1) tc::tc_commit(bar + ACCFULL + (MODE == DQ ? ab : gu & 1));
+                        if (u == nu - 1) tc::tc_commit(bar + ACCFULL + (MODE == DQ ? 0 : gu & 1));
                     }
                     __syncwarp();
                 }
@@ -419,11 +411,9 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             if (!in) return;
             const int h = w.hk * a.G + g;
             un = a.u[((long long)w.b * a.Hq + h) * a.Lq + i];
-            if (!EXACT) {
-                const uint4* po = reinterpret_cast<const uint4*>(a.o.at<__nv_bfloat16>(w.b, h, i) + 16 * q4);
-                orow[0] = po[0];
-                orow[1] = po[1];
-            }
+            const uint4* po = reinterpret_cast<const uint4*>(a.o.at<__nv_bfloat16>(w.b, h, i) + 16 * q4);
+            orow[0] = po[0];
+            orow[1] = po[1];
         };
         if (MODE == DQ && begin_item(0)) ask(items[0]);
         for (int it = 0; ok && begin_item(it); ++it) {
@@ -443,7 +433,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                     ur = un * uscale;
                 }
                 if (!ctl.wait_warp(RFULL + rb, (it >> 1) & 1)) break;
-                if (!EXACT) {  // D = dO . O, a quarter of the channels here
+                {  // dO . O, a quarter of the channels here
                     const uint8_t* dO = sm + OFF_R + (2 * rb + 1) * TILE;
                     float x = 0.f;
 #pragma unroll
@@ -472,18 +462,9 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             const int alo = __reduce_min_sync(~0u, hi < lo ? 0x7fffffff : lo);
             const int ahi = __reduce_max_sync(~0u, hi < lo ? -1 : hi);
             // This team's units: every second one of the block's.  c: the unit's chunk.
-            float sum = 0.f;  // EXACT: of P G
-            bool summed = !EXACT || n == 0;
+            uint64_t sum2 = 0;  // DQ: of P (G - D), two columns apart
             int c = (gu ^ team) & 1;
-            for (int u = c;; u += 2, c += 2) {
-                if (EXACT && !summed && u >= n) {  // the first pass is over
-                    if (!share_d(sum, D)) {
-                        ok = false;
-                        break;
-                    }
-                    summed = true;
-                }
-                if (u >= nu) break;
+            for (int u = c; u < nu; u += 2, c += 2) {
                 while (c >= n) c -= n;
                 const int gv0 = gu + u, s = gv0 % NST, x = gv0 % NSLOT;
                 if ((a.mask && !ctl.wait_warp(READY + s, (gv0 / NST) & 1)) ||
@@ -497,15 +478,10 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                 uint32_t on = a.mask ? words[2 * s + hf] : ~0u;
                 const bool full = j0 >= wlo && j0 + 31 <= whi && on == ~0u;
                 const bool any = j0 <= ahi && j0 + 31 >= alo;
-                const bool only_sum = EXACT && !summed;
-                uint32_t pw[MODE == DKV ? 16 : 1], dw[16];
+                uint32_t pw[16], dw[16];
                 if (!any) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) dw[j] = 0u;
-                    if constexpr (MODE == DKV) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) pw[j] = 0u;
-                    }
+                    for (int j = 0; j < 16; ++j) pw[j] = dw[j] = 0u;
                 } else {
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {  // 16 columns at a time
@@ -537,28 +513,30 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                             tc::upk2(x2, e0, e1);
                             e0 = ex2(e0);
                             e1 = ex2(e1);
-                            tc::upk2(mul2(d2, tc::pk2(e0, e1)), d0, d1);
-                            if (EXACT && only_sum) sum += d0 + d1;
+                            d2 = mul2(d2, tc::pk2(e0, e1));
+                            if (MODE == DQ) sum2 = tc::add2(sum2, d2);
+                            tc::upk2(d2, d0, d1);
                             dw[8 * z + j] = tc::pack_bf16(d0, d1);
-                            if constexpr (MODE == DKV) pw[8 * z + j] = tc::pack_bf16(e0, e1);
+                            pw[8 * z + j] = tc::pack_bf16(e0, e1);
                         }
                     }
                 }
-                if (!only_sum) {
-                    if constexpr (MODE == DKV) {
-                        tc::tmem_st16(mS, pw);
-                        tc::tmem_st16(mG, dw);
-                    } else {
-                        tc::tmem_st16(mS, dw);
-                    }
-                    tc::tmem_wait_st();
-                }
+                tc::tmem_st16(mS, pw);
+                tc::tmem_st16(mG, dw);
+                tc::tmem_wait_st();
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bar + DSFULL + x);
             }
             if (!ok) break;
             gu += nu;
+            float rest = 0.f;  // DQ: what D lacked
+            if (MODE == DQ) {
+                float x0, x1;
+                tc::upk2(sum2, x0, x1);
+                if (!share_d(x0 + x1, rest)) break;
+                D += rest;
+            }
             if (MODE == DQ && exists && q4 == 0) {  // for the key sweep: u / c and -D
                 uint32_t u0, u1, u2, d0, d1, d2;
                 split3(ur, u0, u1, u2);
@@ -569,10 +547,9 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             if (MODE == DQ && begin_item(it + 1)) ask(items[(it + 1) % NIT]);
             // The accumulators, this warp's lanes.  DQ: 16 columns.  DKV: 32 of each,
             // by the team that had the last unit; the other is at the next item.
-            const int ab = na % NACC;
             const bool mine = MODE == DQ || (((nu > 0 ? gu - 1 : 0) ^ team) & 1) == 0;
-            if (nu > 0 && mine) {  // ACCFULL: one per buffer (DQ), per team (DKV)
-                if (!ctl.wait_warp(ACCFULL + (MODE == DQ ? ab : team), (na / NACC) & 1)) break;
+            if (nu > 0 && mine) {  // DKV: a barrier per team
+                if (!ctl.wait_warp(ACCFULL + (MODE == DQ ? 0 : team), na & 1)) break;
                 ++na;
                 tc::tc_fence_after();
             }
@@ -580,10 +557,16 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
 #pragma unroll
                 for (int k = 0; k < (MODE == DQ ? 1 : 4); ++k) {
                     const int col = MODE == DQ ? 16 * q4 : 32 * hf + 16 * (k & 1);
-                    uint32_t o[16];
+                    uint32_t o[16], pk[MODE == DQ ? 16 : 1];
                     if (nu > 0) {
-                        tc::tmem_ld16(tA + 64 * (MODE == DQ ? ab : k >> 1) + lanebase + col, o);
+                        tc::tmem_ld16(tA + (MODE == DQ || k > 1 ? 64 : 0) + lanebase + col, o);
+                        if constexpr (MODE == DQ) tc::tmem_ld16(tA + lanebase + col, pk);
                         tc::tmem_wait_ld();
+                        if constexpr (MODE == DQ) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                o[j] = __float_as_uint(fmaf(-rest, __uint_as_float(pk[j]), __uint_as_float(o[j])));
+                        }
                     }
                     const float f = MODE == DKV && k < 2 ? 1.f : a.c;
                     if (exists) {
@@ -606,7 +589,7 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                 if (nu > 0) {
                     tc::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(bar + ACCEMPTY + ab);
+                    if (lane == 0) tc::mbar_arrive(bar + ACCEMPTY);
                 }
             }
             end_item(it);
