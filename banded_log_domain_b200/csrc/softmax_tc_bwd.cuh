@@ -390,11 +390,13 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
         bool ok = true;
         // The sum over the four warps that hold a row's columns.  Two buffers: to
         // reach the one after the next, every warp has read this one.
-        auto share_d = [&](float x, float& total) -> bool {
-            float* sh = xd + (nx & 1) * 512;
-            sh[q4 * 128 + r] = x;
+        auto put = [&](float x) {
+            xd[(nx & 1) * 512 + q4 * 128 + r] = x;
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(bar + XDSUM);
+        };
+        auto get = [&](float& total) -> bool {
+            const float* sh = xd + (nx & 1) * 512;
             if (!ctl.wait_warp(XDSUM, nx & 1)) return false;
             ++nx;
             total = (sh[r] + sh[128 + r]) + (sh[256 + r] + sh[384 + r]);
@@ -447,7 +449,8 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                             x = fmaf(f.x, k.x, fmaf(f.y, k.y, x));
                         }
                     }
-                    if (!share_d(in ? x : 0.f, D)) break;
+                    put(in ? x : 0.f);
+                    if (!get(D)) break;
                 }
                 if (lane == 0) tc::mbar_arrive(bar + REMPTY + rb);
             } else if (exists && a.live(w.b, i)) {
@@ -534,17 +537,9 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
             if (MODE == DQ) {
                 float x0, x1;
                 tc::upk2(sum2, x0, x1);
-                if (!share_d(x0 + x1, rest)) break;
-                D += rest;
+                put(x0 + x1);
+                if (begin_item(it + 1)) ask(items[(it + 1) % NIT]);
             }
-            if (MODE == DQ && exists && q4 == 0) {  // for the key sweep: u / c and -D
-                uint32_t u0, u1, u2, d0, d1, d2;
-                split3(ur, u0, u1, u2);
-                split3(-D, d0, d1, d2);
-                a.aug[2 * at] = make_uint4(u0 | u1 << 16, u2 | d0 << 16, d1 | d2 << 16, 0u);
-                a.aug[2 * at + 1] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            if (MODE == DQ && begin_item(it + 1)) ask(items[(it + 1) % NIT]);
             // The accumulators, this warp's lanes.  DQ: 16 columns.  DKV: 32 of each,
             // by the team that had the last unit; the other is at the next item.
             const bool mine = MODE == DQ || (((nu > 0 ? gu - 1 : 0) ^ team) & 1) == 0;
@@ -552,6 +547,16 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                 if (!ctl.wait_warp(ACCFULL + (MODE == DQ ? 0 : team), na & 1)) break;
                 ++na;
                 tc::tc_fence_after();
+            }
+            if (MODE == DQ) {
+                if (!get(rest)) break;
+                if (exists && q4 == 0) {  // for the key sweep: u / c and -D
+                    uint32_t u0, u1, u2, d0, d1, d2;
+                    split3(ur, u0, u1, u2);
+                    split3(-(D + rest), d0, d1, d2);
+                    a.aug[2 * at] = make_uint4(u0 | u1 << 16, u2 | d0 << 16, d1 | d2 << 16, 0u);
+                    a.aug[2 * at + 1] = make_uint4(0u, 0u, 0u, 0u);
+                }
             }
             if (mine) {
 #pragma unroll
