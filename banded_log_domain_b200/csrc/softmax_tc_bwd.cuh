@@ -481,14 +481,14 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                 uint32_t on = a.mask ? words[2 * s + hf] : ~0u;
                 const bool full = j0 >= wlo && j0 + 31 <= whi && on == ~0u;
                 const bool any = j0 <= ahi && j0 + 31 >= alo;
-                uint32_t pw[16], dw[16];
                 if (!any) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) pw[j] = dw[j] = 0u;
+                    const uint32_t zero[16] = {};
+                    tc::tmem_st16(mS, zero);
+                    tc::tmem_st16(mG, zero);
                 } else {
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {  // 16 columns at a time
-                        uint32_t sv[16], gv[16];
+                        uint32_t sv[16], gv[16], pw[8], dw[8];
                         tc::tmem_ld16(mS + 16 * z, sv);
                         tc::tmem_ld16(mG + 16 * z, gv);
                         tc::tmem_wait_ld();
@@ -519,13 +519,14 @@ __global__ void __launch_bounds__(THREADS, 1) tc_bwd(const Args a, const __grid_
                             d2 = mul2(d2, tc::pk2(e0, e1));
                             if (MODE == DQ) sum2 = tc::add2(sum2, d2);
                             tc::upk2(d2, d0, d1);
-                            dw[8 * z + j] = tc::pack_bf16(d0, d1);
-                            pw[8 * z + j] = tc::pack_bf16(e0, e1);
+                            dw[j] = tc::pack_bf16(d0, d1);
+                            pw[j] = tc::pack_bf16(e0, e1);
                         }
+                        // over columns that this thread has read
+                        tmem_st8(mS + 8 * z, pw);
+                        tmem_st8(mG + 8 * z, dw);
                     }
                 }
-                tc::tmem_st16(mS, pw);
-                tc::tmem_st16(mG, dw);
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 __syncwarp();
