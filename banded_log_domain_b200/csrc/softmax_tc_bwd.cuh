@@ -16,24 +16,25 @@
 // A unit is one row tile times one chunk.  S and G of a unit go to one of three
 // slots of TMEM; a team of eight warps (two per lane quadrant, 32 columns each)
 // reads them, forms P and dS and writes them as bf16 over the S and G they came
-// from, from where the second products read them as their A operand.  Two teams
-// take the units in turn; in DQ they ask for their rows of the next item while one
-// ends (32768 tokens of 16 heads, W = 256: 0.53 -> 0.51 ms for both sweeps), in DKV
-// one writes an item's gradients while the other begins the next (0.51 -> 0.49 ms;
-// DQ's teams form D together, and apart took longer).  (The row tiles' operands in
-// TMEM as well made the MMAs shorter but left five buffers of S or G in DKV and one
-// accumulator in DQ: 3 % slower.)  A banded item is bound by its start and its end,
-// where the products drain; a long one by the hand-overs (without any exponentials
-// 8192 dense tokens of 8 heads took 596 us for 643).  One warp issues S and G,
-// another the second products
-// (one thread for all that add into an accumulator); a loader brings the tiles,
-// and an aux warp prepares each chunk's columns (mask words; zeroed operand rows
-// of tokens that are not in use, as 0 times what they hold need not be 0).  In DKV
-// u and D belong to columns: they enter S and G in the products themselves, as 16
-// more channels, u / c and -D in three bf16 parts each (2^-24 of them) against
-// ones (read by every thread from shared memory they cost the teams twice the
-// time, behind the products' own reads).  D = dO . O is formed by the teams' warps
-// at an item's start, a quarter of the channels each.
+// from, 16 columns at a time (32 at once spilled: 0.55 ms for 0.48 at 32768 tokens
+// of 16 heads, W = 256), from where the second products read them as their A
+// operand.  Two teams take the units in turn; in DQ they ask for their rows of the
+// next item while one ends (0.53 -> 0.51 ms), in DKV one writes an item's gradients
+// while the other begins the next (0.51 -> 0.49 ms; DQ's teams form D together, and
+// apart took longer).  One warp issues S and G, another the second products (one
+// thread for all that add into an accumulator); a loader brings the tiles, and an
+// aux warp prepares each chunk's columns (mask words; zeroed operand rows of tokens
+// that are not in use, as 0 times what they hold need not be 0).  In DKV u and D
+// belong to columns: they enter S and G in the products themselves, as 16 more
+// channels, u / c and -D in three bf16 parts each (2^-24 of them) against ones
+// (read by every thread from shared memory they cost the teams twice the time).
+// dO . O is formed by the teams' warps at an item's start, a quarter of the channels
+// each.
+//
+// 8192 dense tokens of 8 heads take 651 us for the eight products, 0.52 of the
+// matrix rate.  A banded item is bound by its start and its end, where the products
+// drain, a long one by the hand-overs.  (The row tiles' operands in TMEM as well
+// made the MMAs shorter but left five buffers of S or G in DKV: 3 % slower.)
 #pragma once
 
 #include "softmax_tc.cuh"
