@@ -211,15 +211,19 @@ sa_status sinkhorn_attn_rotary_freqs(int rot, double base, sa_rotary_scaling kin
         auto at = [&](double turns) {
             return n * std::log(train_len / (turns * 2.0 * 3.14159265358979323846)) / std::log(base);
         };
+        // The ramp starts at the first pair at the earliest, but may end behind the
+        // last (YaRN's bound is rot - 1): pairs that still turn more than turns_lo
+        // times are mixed, not divided by the whole factor.
         lo = std::max(0.0, std::floor(at(turns_hi)));
-        hi = std::min(n - 1.0, std::ceil(at(turns_lo)));
+        hi = std::min(rot - 1.0, std::ceil(at(turns_lo)));
     }
     if (kind == SA_ROTARY_NTK && n > 1) base *= std::pow(factor, (double)n / (n - 1));
     for (int i = 0; i < n; ++i) {
         double f = std::pow(base, -(double)i / n);
         if (kind == SA_ROTARY_LINEAR) f /= factor;
         if (kind == SA_ROTARY_BY_PARTS) {
-            const double ramp = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 1e-3)));
+            // (hi <= lo: every pair lies on one side of the ramp)
+            const double ramp = hi > lo ? std::min(1.0, std::max(0.0, (i - lo) / (hi - lo))) : i >= hi ? 1.0 : 0.0;
             f = f / factor * ramp + f * (1.0 - ramp);
         }
         freqs[i] = f;

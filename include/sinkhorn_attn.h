@@ -469,7 +469,8 @@ typedef enum {
     SA_ROTARY_NTK = 2,       /* base replaced by base * factor^(rot / (rot - 2)) */
     SA_ROTARY_BY_PARTS = 3   /* YaRN: pairs that turn more than turns_hi times over
                                 train_len tokens are kept, fewer than turns_lo divided
-                                by factor, a linear mix in the pair index between */
+                                by factor, a linear mix in the pair index between (the
+                                indices rounded outwards and held to 0 .. rot - 1) */
 } sa_rotary_scaling;
 
 /* Host-only arithmetic (no device work): writes freqs[0 .. rot/2) (host) in

@@ -137,6 +137,31 @@ def test_rotary_frequencies():
     assert one.tolist() == [1.0]
 
 
+# train_len from far too short for any turn to long enough that even the slowest pair
+# turns more than turns_lo times (65536, 131072) or turns_hi times (2^22)
+@pytest.mark.parametrize("rot", [2, 6, 64])
+@pytest.mark.parametrize("train_len", [3, 6, 7, 100, 512, 4096, 65536, 131072, 1 << 22])
+@pytest.mark.parametrize("turns", [(32.0, 1.0), (8.0, 2.0)])
+def test_frequencies_by_parts_over_all_trained_lengths(rot, train_len, turns):
+    factor, n = 8.0, rot // 2
+    got, _ = sa.sinkhorn_attn_rotary_freqs(rot, scaling="by_parts", factor=factor, train_len=train_len,
+                                           turns=turns, device="cpu")
+    f, _ = sa.sinkhorn_attn_rotary_freqs(rot, device="cpu")
+    # the pair index at which train_len tokens make t whole turns: base^(-i/n) train_len = 2 pi t
+    at = [n * math.log(train_len / (2 * math.pi * t), 10000.0) for t in turns]
+    start, end = max(0, math.floor(at[0])), min(rot - 1, math.ceil(at[1]))
+    for i in range(n):
+        count = float(f[i]) * train_len / (2 * math.pi)
+        share = float(got[i] / f[i])
+        if count > turns[0]:
+            assert abs(share - 1) < 1e-13
+        elif count < turns[1]:
+            assert abs(share * factor - 1) < 1e-13
+        else:
+            ramp = (i - start) / (end - start)
+            assert 0 <= ramp <= 1 and abs(share - (ramp / factor + 1 - ramp)) < 1e-13
+
+
 @pytest.mark.parametrize("kw", [
     dict(rot=0), dict(rot=7), dict(rot=8, base=1.0), dict(rot=8, base=float("inf")),
     dict(rot=8, factor=0.5), dict(rot=8, factor=float("nan")),
