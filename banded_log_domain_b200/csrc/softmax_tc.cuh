@@ -142,6 +142,15 @@ constexpr int REG_SOFTMAX = 104, REG_OTHER = 64;
 static_assert(512 * REG_SOFTMAX + 128 * REG_OTHER <= 61440, "register split");
 constexpr int KT = TILE / 2;  // one 64 x 64 bf16 tile of keys or values
 constexpr int NIT = 4;        // items in flight between the loader and the other warps
+// fma(S, c2, -m) takes m's rounding, half a step, into every exponent of a row: it
+// cancels between P and its sum while it is at most 1/2.  From kRound on a row's
+// products are rounded as m was and then subtracted, so that the largest gives 1,
+// whatever its size.  (By row: the groups that share its keys then do the same.)
+// A warp that holds such a row takes kBig for the first key that all its rows
+// attend, and with it none of its words for a whole one: the test stands where masks
+// are looked at (beside the unmasked words it took 4 to 9 % of the kernel's time).
+constexpr float kRound = 0x1p24f;
+constexpr int kBig = 0x7fffffff;
 
 // What every role needs of an item; the loader writes it, once per block.
 struct Item {
@@ -462,7 +471,8 @@ __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_
             }
             const bool dead = __all_sync(~0u, hi < lo);  // no row of this warp attends anything
             // keys that every row of the warp attends, masks aside
-            const int wlo = __reduce_max_sync(~0u, lo), whi = __reduce_min_sync(~0u, hi);
+            const int whi = __reduce_min_sync(~0u, hi);
+            int wlo = __reduce_max_sync(~0u, lo);  // (kBig: see below)
             float m = -INFINITY;  // running maximum (log2 units), moved in steps of more than 8
             uint64_t l2[2] = {0, 0};
             bool some = false, used = false;
@@ -488,7 +498,8 @@ __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_
                         on[0] = wd.x;
                         on[1] = wd.y;
                     }
-                    const bool full = j0 >= wlo && j0 + 63 <= whi && (on[0] & on[1]) == ~0u;
+                    const bool live[2] = {on[0] == ~0u, on[1] == ~0u};
+                    bool full = j0 >= wlo && j0 + 63 <= whi && live[0] && live[1];
                     if (!full) {
 #pragma unroll
                         for (int k = 0; k < 2; ++k) on[k] &= range_bits(lo - j0 - 32 * k, hi - j0 - 32 * k);
@@ -518,6 +529,10 @@ __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_
                     if (__any_sync(~0u, move)) {
                         const float f = move ? ex2(m - mx) : 1.f;  // 0 from an empty row
                         if (move) m = mx;
+                        if (__any_sync(~0u, fabsf(m) >= kRound && fabsf(m) < INFINITY)) {
+                            wlo = kBig;  // no word is taken as a whole from here on
+                            full = false;
+                        }
                         float y, z;
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
@@ -547,7 +562,8 @@ __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_
                         uint32_t pw[16];
                         load(k);
                         // a word of 32 columns is in use for all rows, for none, or for some
-                        const bool all = full || __all_sync(~0u, on[k] == ~0u);
+                        const bool all =
+                            full || (live[k] && j0 + 32 * k >= wlo && j0 + 32 * k + 31 <= whi);
                         if (all) {
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
@@ -561,6 +577,16 @@ __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_
                                     e0 = ex2(e0);
                                     e1 = ex2(e1);
                                 }
+                                l2[j & 1] = tc::add2(l2[j & 1], tc::pk2(e0, e1));
+                                pw[j] = tc::pack_bf16(e0, e1);
+                            }
+                        } else if (wlo == kBig) {
+                            const bool round = fabsf(use) >= kRound;
+                            const float pre = round ? a.c2 : 1.f, post = round ? 1.f : a.c2;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float e0 = ex2(fmaf(__uint_as_float(sv[2 * j]) * pre, post, use));
+                                const float e1 = ex2(fmaf(__uint_as_float(sv[2 * j + 1]) * pre, post, use));
                                 l2[j & 1] = tc::add2(l2[j & 1], tc::pk2(e0, e1));
                                 pw[j] = tc::pack_bf16(e0, e1);
                             }

@@ -391,6 +391,10 @@ sa_status sinkhorn_attn_bias_certificate(int n_depths, const int* depths, int n_
  *     (the unwritten tail of a cache), are not used, whatever they hold.  A
  *     non-finite value of a token in use reaches the rows that attend it and
  *     may reach others whose tokens lie within 255 positions of those.
+ *   - Scores of any size that fp32 holds give finite O and u.  The backward forms
+ *     P = exp(S + u) from the fp32 u, whose rounding is a factor of up to
+ *     1 +- 2^-21 |u| on P: gradients take an error of that size and mean nothing
+ *     from |u| of about 2^20 on.
  *   - Results do not depend on the order in which blocks run (no atomics).
  *   - The workspace needs no initialisation: every call resets the status word
  *     at its start (read it with sinkhorn_attn_poll), so calls on two streams

@@ -121,6 +121,35 @@ def test_temperatures_far_from_one(dtype, eps):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("log2_eps", [-10, -20, -24, -28, -30, -33, -40, -60, -100])
+@pytest.mark.parametrize("Hq,Lq,Lk,W", [(2, 200, 200, 200), (2, 300, 300, 40), (4, 40, 3000, 3000), (2, 1, 3000, 3000),
+                                        (16, 2500, 2500, 60)])
+def test_scores_of_any_size(dtype, log2_eps, Hq, Lq, Lk, W):
+    # Small whole numbers and a power of two for c: <q, k> is exact and differs by 1
+    # at least, S by 2^10 / 8, so P is 1 / (keys that share the maximum) and 0
+    # elsewhere, for scores of up to 2^9 2^97.  O errs as bounds() says, with s = 0 in
+    # it.  u = -(max S + ln ties): its constants, products and sum round six times.
+    import banded_log_domain_b200 as sa
+
+    g = torch.Generator(device="cuda").manual_seed(Lk)
+    r = lambda h, n: torch.randint(-3, 4, (1, h, n, 64), generator=g, device="cuda").to(dtype)
+    q, k = r(Hq, Lq), r(2, Lk)
+    v = torch.randn(1, 2, Lk, 64, generator=g, device="cuda").to(dtype)
+    eps = 2.0 ** log2_eps
+    o, u = sa.sinkhorn_attn_softmax_fwd(q, k, v, W=W, eps=eps, causal=True)
+    kk, vv = (t.double().repeat_interleave(Hq // 2, 1) for t in (k, v))
+    S = q.double() @ kk.transpose(-1, -2)
+    S.masked_fill_(~ref.support(1, Lq, Lk, W, True, None, None, "cuda")[:, None], -float("inf"))
+    top = S.amax(-1, keepdim=True)
+    ties = (S == top).double()
+    P = ties / ties.sum(-1, keepdim=True)
+    ref.close("o", o, P @ vv, (ref.H[dtype] + ref.S) * (P @ vv.abs()), dtype)
+    want = -(top[..., 0] / (8 * eps) + torch.log(ties.sum(-1)))
+    assert bool(torch.isfinite(u).all())
+    assert bool(((u.double() - want).abs() <= 6 * 2.0 ** -24 * want.abs() + ref.U_ATOL).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("G", [1, 4, 7])
 @pytest.mark.parametrize("Lq,Lk,W", [(1, 1, 0), (1, 70, 70), (1, 1000, 1000), (1, 5000, 5000), (1, 5000, 300),
                                      (2, 130, 130), (5, 4096, 4096), (17, 3001, 3001), (40, 3001, 900)])
