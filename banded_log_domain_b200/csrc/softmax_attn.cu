@@ -130,6 +130,12 @@ bool view(sm::View* v, const void* ptr, const long long s[3], int B, int H, int 
     return true;
 }
 
+// A call with nothing to do launches no kernel that would reset the status word.
+sa_status reset_status(void* ws, void* stream) {
+    if (!device_ok(ws)) return SA_OK;  // an empty call needs no workspace
+    return cudaMemsetAsync(ws, 0, 4, (cudaStream_t)stream) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+}
+
 bool ints_ok(const int* x) { return !x || (((uintptr_t)x & 3u) == 0 && on_current_device(x)); }
 
 // Every kernel here is launched with programmatic stream serialisation and waits
@@ -335,7 +341,7 @@ sa_status sinkhorn_attn_softmax_fwd(const sa_softmax_params* p, const void* q, c
     if (!view(&a.q, q, p->q_stride, p->B, p->Hq, p->Lq, size) || !view(&a.k, k, p->k_stride, p->B, p->Hk, p->Lk, size) ||
         !view(&a.v, v, p->v_stride, p->B, p->Hk, p->Lk, size) || !view(&a.o, o, p->o_stride, p->B, p->Hq, p->Lq, size))
         return SA_ERR_INVALID_ARG;
-    if (pl.rows == 0) return SA_OK;
+    if (pl.rows == 0) return reset_status(ws, stream);
     if (!device_ok(q) || !device_ok(k) || !device_ok(v) || !device_ok(o) || !device_ok(u) || !device_ok(ws) ||
         !mask_ok(mask) || !ints_ok(q_pos))
         return SA_ERR_INVALID_ARG;
@@ -369,7 +375,7 @@ sa_status sinkhorn_attn_softmax_bwd(const sa_softmax_params* p, const void* q, c
         !view(&a.dk, dk, p->dk_stride, p->B, p->Hk, p->Lk, size) ||
         !view(&a.dv, dv, p->dv_stride, p->B, p->Hk, p->Lk, size))
         return SA_ERR_INVALID_ARG;
-    if ((long long)p->B * p->Hk * p->Lk == 0) return SA_OK;
+    if ((long long)p->B * p->Hk * p->Lk == 0) return reset_status(ws, stream);
     if (!device_ok(k) || !device_ok(v) || !device_ok(dk) || !device_ok(dv) || !device_ok(ws) || !mask_ok(mask) ||
         !ints_ok(q_pos))
         return SA_ERR_INVALID_ARG;

@@ -357,6 +357,20 @@ def test_workspace_status_and_reuse():
     assert e.value.status == -3
 
 
+@pytest.mark.parametrize("B,H,Lq,Lk", [(1, 2, 0, 0), (1, 2, 0, 5), (0, 2, 3, 3), (2, 0, 3, 5)])
+def test_empty_calls_reset_the_status_word(B, H, Lq, Lk):
+    import banded_log_domain_b200 as sa
+
+    q, k, v, dO = draw(BF16, B, H, H, Lq, Lk)
+    u = torch.empty(B, H, Lq, device="cuda")
+    for f in (lambda ws: sa.sinkhorn_attn_softmax_fwd(q, k, v, W=1, ws=ws),
+              lambda ws: sa.sinkhorn_attn_softmax_bwd(q, k, v, q, dO, u, W=1, ws=ws)):
+        ws = torch.full((1024,), 0x5a, dtype=torch.uint8, device="cuda")
+        f(ws)
+        assert sa.sinkhorn_attn_poll(ws) == 0
+        f(None)
+
+
 def test_refusals_on_the_gpu():
     import banded_log_domain_b200 as sa
 
