@@ -715,8 +715,9 @@ def _softmax_params(q, k, v, W, eps, causal):
         raise ValueError(f"k: {tuple(shape)} does not go with q {tuple(q.shape)}")
     _same("k", k, q, shape)
     _same("v", v, q, shape)
-    p = sa_softmax_params(B, Hq, shape[1], Lq, shape[2], d, min(int(W), 2**31 - 1), float(eps),
-                          1 if causal else 0, _DTYPES[q.dtype])
+    # (a band past 2^31 is dense, and one below -2^31 must not wrap around to one)
+    p = sa_softmax_params(B, Hq, shape[1], Lq, shape[2], d, max(-1, min(int(W), 2**31 - 1)),
+                          float(eps), 1 if causal else 0, _DTYPES[q.dtype])
     _strided(p, "q", q)
     _strided(p, "k", k)
     _strided(p, "v", v)

@@ -371,6 +371,24 @@ def test_empty_calls_reset_the_status_word(B, H, Lq, Lk):
         f(None)
 
 
+@pytest.mark.parametrize("W", [-1, -2 ** 31, -2 ** 31 - 1, -2 ** 32, -2 ** 40])
+def test_negative_bands_are_refused(W):
+    import banded_log_domain_b200 as sa
+
+    q, k, v, _ = draw(F32, 1, 1, 1, 8, 8)
+    with pytest.raises(sa.SinkhornAttnError) as e:
+        sa.sinkhorn_attn_softmax_fwd(q, k, v, W=W)
+    assert e.value.status == -1
+
+
+def test_bands_past_32_bits_are_dense():
+    import banded_log_domain_b200 as sa
+
+    q, k, v, _ = draw(F32, 1, 1, 1, 8, 8)
+    a, b = (sa.sinkhorn_attn_softmax_fwd(q, k, v, W=W) for W in (8, 2 ** 40))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_refusals_on_the_gpu():
     import banded_log_domain_b200 as sa
 
