@@ -1,5 +1,7 @@
 """Softmax attention and rotary positions on a GPU against the float64 forms,
 within bounds that count roundings (tests/softmax_ref.py)."""
+import math
+
 import pytest
 import torch
 
@@ -479,6 +481,34 @@ def test_rotary_layouts_in_place_and_undone(dtype, rot, interleaved):
     for x, y in zip((q, k), back):
         n = float(x.double().abs().max())
         assert float((x.double() - y.double()).abs().max()) <= 4 * h * n + 2.0 ** -18 * n
+
+
+@pytest.mark.parametrize("inverse", [False, True])
+def test_cosines_and_sines_at_far_positions(inverse):
+    # Channel pairs of (1, 0) give the cosine and the sine themselves.  They err by
+    # sincospif's one ulp (2^-23 at most), the half steps of the remainder's correction,
+    # of the scale (1 here) and of the product with 1: 5 2^-24, and less than 2^-40 of
+    # the angle.  The exact angle: whole numbers, with 2 pi to 60 digits.
+    from fractions import Fraction as F
+
+    import banded_log_domain_b200 as sa
+
+    two_pi = 2 * F(314159265358979323846264338327950288419716939937510582097494459, 10 ** 62)
+    freqs, _ = sa.sinkhorn_attn_rotary_freqs(16)
+    at = [0, 1, 2, 1000, 2 ** 20 - 3, 2 ** 27 + 1, 1_000_000_007, 2 ** 31 - 1, -2 ** 31] + \
+        [2 ** 31 - 1 - 12345 * i for i in range(1, 400)]
+    pos = torch.tensor([at], dtype=torch.int32, device="cuda")
+    q = torch.zeros(1, 1, len(at), 16, device="cuda")
+    q[..., :8] = 1
+    f = sa.sinkhorn_attn_rotary_bwd if inverse else sa.sinkhorn_attn_rotary_fwd
+    y = f(q, None, freqs, pos=pos)[0][0, 0].double().cpu()
+    want = torch.empty(len(at), 16, dtype=torch.float64)
+    for t, p in enumerate(at):
+        for i, w in enumerate(freqs.tolist()):
+            a = F(-p if inverse else p) * F(w)
+            a = float(a - two_pi * round(a / two_pi))
+            want[t, i], want[t, 8 + i] = math.cos(a), math.sin(a)
+    assert float((y - want).abs().max()) <= 5 * 2.0 ** -24
 
 
 def test_rotary_is_relative():
