@@ -566,3 +566,19 @@ def test_a_layer_rotary_attention_and_back(dtype):
         v2 = v.repeat_interleave(Hq // Hk, 1)
         so, st = sa.sinkhorn_attn_fwd(rq, rk2, v2, W=64, eps=1.0, T=2, R=2)
         assert bool(torch.isfinite(so).all()) and bool(torch.isfinite(st).all())
+
+
+def test_the_readme_runs():
+    # its Python examples, one after the other as a reader would type them
+    import os
+    import re
+
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as f:
+        blocks = re.findall(r"```python\n(.*?)```", f.read(), re.S)
+    assert len(blocks) >= 2
+    names = {}
+    for block in blocks:
+        exec(block, names)
+    for n in ("o", "u", "dq", "dk", "dv"):
+        assert bool(torch.isfinite(names[n]).all())
+    assert names["dq"].shape == names["q"].shape and names["dk"].shape == names["k"].shape
