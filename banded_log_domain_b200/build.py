@@ -5,9 +5,11 @@
 from __future__ import annotations
 
 import glob
+import json
 import os
 import subprocess
 import sys
+import time
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -28,27 +30,45 @@ def sources():
 
 
 DEBUG_LIB = os.path.join(PKG, "libsinkhorn_attn_debug.so")
-OBJ = os.path.join(ROOT, "build")  # object files and their dependency lists, one folder per library
+OBJ = os.path.join(ROOT, "build")  # object files and how they were made, one folder per library
+TMP = f".tmp{os.getpid()}"
 
 
-def deps(dep_file: str):
-    """The files an object was compiled from, as nvcc listed them (None: never compiled)."""
-    if not os.path.exists(dep_file):
-        return None
+def dep_list(dep_file: str):
+    """The files that a compilation read, as nvcc listed them."""
     with open(dep_file) as f:
         return f.read().replace("\\\n", " ").split(":", 1)[1].split()
 
 
-def stale(target: str, files) -> bool:
-    if files is None or not os.path.exists(target):
-        return True
-    t = os.path.getmtime(target)
-    return any(not os.path.exists(f) or os.path.getmtime(f) > t for f in files)
+def current(target: str, record: str, cmd) -> bool:
+    """Whether ``target`` was made by ``cmd`` from files that have not changed since:
+    by what ``record`` says, which is written when the target is complete."""
+    try:
+        with open(record) as f:
+            r = json.load(f)
+        t = os.path.getmtime(target)
+        return r["cmd"] == cmd and all(os.path.getmtime(f) <= t for f in r["files"])
+    except (OSError, ValueError, KeyError):
+        return False
+
+
+def put(target: str, record: str, tmp: str, cmd, files, began: float):
+    """``tmp`` becomes ``target``, as old as the command's start (a source written while
+    it ran is newer), and the record says how it was made."""
+    os.utime(tmp, (began, began))
+    if os.path.exists(record):
+        os.remove(record)
+    os.replace(tmp, target)
+    with open(record + TMP, "w") as f:
+        json.dump({"cmd": cmd, "files": files}, f)
+    os.replace(record + TMP, record)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Builds the library and its bounds-checked debug twin (-DSA_DEBUG): the
-    stale sources compiled side by side, then linked."""
+    stale sources compiled side by side, then linked.  Everything is written under
+    a name of this process and then renamed, so that a build that is killed, or
+    another at the same time, leaves nothing half-written behind."""
     jobs, links = [], []
     for lib, extra, sub in ((LIB, [], "release"), (DEBUG_LIB, ["-DSA_DEBUG"], "debug")):
         out = os.path.join(OBJ, sub)
@@ -57,27 +77,35 @@ def build(force: bool = False, verbose: bool = False) -> str:
         for src in sources():
             obj = os.path.join(out, os.path.splitext(os.path.basename(src))[0] + ".o")
             objs.append(obj)
-            if force or stale(obj, deps(obj + ".d")):
-                cmd = [NVCC, *FLAGS, *extra, "-c", "-MD", "-MF", obj + ".d", "-o", obj, src]
+            cmd = [NVCC, *FLAGS, *extra, "-c", src]
+            if force or not current(obj, obj + ".json", cmd):
+                run = cmd + ["-MD", "-MF", obj + ".d" + TMP, "-o", obj + TMP]
                 if verbose:
-                    print(" ".join(cmd), flush=True)
-                jobs.append((cmd, obj, subprocess.Popen(cmd)))
-        links.append((lib, objs))
-    failed = [obj for _, obj, p in jobs if p.wait() != 0]
-    for obj in failed:  # nothing half-written is taken for current
-        if os.path.exists(obj):
-            os.remove(obj)
-    for cmd, obj, p in jobs:
-        if p.returncode != 0:
-            raise subprocess.CalledProcessError(p.returncode, cmd)
-    for lib, objs in links:
-        if force or stale(lib, objs):
-            tmp = lib + f".tmp{os.getpid()}"
-            cmd = [NVCC, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", "-o", tmp, *objs]
+                    print(" ".join(run), flush=True)
+                jobs.append((cmd, obj, time.time(), subprocess.Popen(run)))
+        links.append((lib, os.path.join(out, "link.json"), objs))
+    for _, _, _, p in jobs:
+        p.wait()
+    failed = None
+    for cmd, obj, began, p in jobs:
+        if p.returncode == 0:
+            put(obj, obj + ".json", obj + TMP, cmd, dep_list(obj + ".d" + TMP), began)
+        else:
+            failed = subprocess.CalledProcessError(p.returncode, cmd)
+        for f in (obj + TMP, obj + ".d" + TMP):
+            if os.path.exists(f):
+                os.remove(f)
+    if failed:
+        raise failed
+    for lib, record, objs in links:
+        cmd = [NVCC, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", *objs]
+        if force or not current(lib, record, cmd):
+            began = time.time()
+            run = cmd + ["-o", lib + TMP]
             if verbose:
-                print(" ".join(cmd), flush=True)
-            subprocess.check_call(cmd)
-            os.replace(tmp, lib)
+                print(" ".join(run), flush=True)
+            subprocess.check_call(run)
+            put(lib, record, lib + TMP, cmd, objs, began)
     return LIB
 
 
