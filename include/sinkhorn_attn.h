@@ -413,8 +413,8 @@ typedef struct {
 
 /* Workspace bytes of the two calls below (either pointer may be NULL).  Both hold
  * 8 bytes per sequence; the backward's 4 (fp32) or 32 (bf16) bytes per query row;
- * and where few rows have their keys split over several blocks, the parts: at
- * most 37 MB in the forward, 10 MB in the fp32 backward. */
+ * and where few rows have their keys split over several blocks, the parts: on 148
+ * SMs at most 20.1 MB in the forward, 9.8 MB in the fp32 backward. */
 sa_status sinkhorn_attn_softmax_workspace_size(const sa_softmax_params* p, size_t* fwd_bytes,
                                                size_t* bwd_bytes);
 

@@ -2,6 +2,7 @@
 GPU tests compare with, argument checks, sizes and the frequencies."""
 import ctypes
 import math
+import random
 
 import pytest
 import torch
@@ -94,6 +95,34 @@ def test_workspace_is_bounded_and_grows_with_the_rows_only():
                 assert f <= 37 << 20 and rows <= b <= rows + (10 << 20)
     f, b = sa.sinkhorn_attn_softmax_workspace_size(P(B=1, Hq=16, Hk=16, Lq=32768, Lk=32768, W=256))
     assert f == 512 and b == 512 + 16 * 32768 * 32
+
+
+def test_the_parts_stay_within_what_the_header_says():
+    # 148 SMs.  Forward: a part of a row is 64 floats and two more, 264 bytes.  Tiled: two
+    # blocks an SM, of 256 rows at most (items of four row tiles are never split);
+    # single tokens: 296 blocks and up to 4096 key heads, 16 rows.  Backward, fp32:
+    # 296 parts of 64 query rows (256 bytes) or 64 key rows (512 bytes).
+    fwd = max(296 * 256, (296 + 4096) * 16) * 264
+    bwd = 296 * 64 * 512
+    assert fwd <= 20.1e6 and bwd <= 9.8e6
+    rng = random.Random(4)
+    log = lambda a, b: int(round(math.exp(rng.uniform(math.log(a), math.log(b)))))
+    for _ in range(20000):
+        dt = rng.choice([sa.SA_F32, sa.SA_BF16])
+        G, B, Hk = (rng.choice(x) for x in ([1, 2, 3, 4, 7, 8, 16, 33, 64], [1, 2, 8, 64, 147], [1, 2, 8, 37, 64]))
+        if B * G * Hk > 65535:
+            continue
+        Lk = log(1, 1 << 30)
+        Lq = min(Lk, log(1, 1 << 16))
+        kw = dict(B=B, Hq=G * Hk, Hk=Hk, Lq=Lq, Lk=Lk, W=rng.choice([Lk, log(1, Lk)]), causal=rng.randint(0, 1), dtype=dt)
+        p = P(**kw)
+        if sa.load().sinkhorn_attn_softmax_workspace_size(ctypes.byref(p), None, None) != 0:
+            continue
+        f, b = sa.sinkhorn_attn_softmax_workspace_size(p)
+        own = B * G * Hk * Lq * (32 if dt == sa.SA_BF16 else 4)
+        head = 256 + (B * 8 + 255) // 256 * 256
+        assert f - head <= fwd + 512, kw  # both arrays of the parts end on 256 bytes
+        assert b - head - own <= (0 if dt == sa.SA_BF16 else bwd) + 512, kw
 
 
 @pytest.mark.parametrize("kw,status", [
