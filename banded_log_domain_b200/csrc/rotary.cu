@@ -5,7 +5,9 @@
 // cosines and sines once, and applies them to the same piece of several heads:
 // the angle p * f is reduced in double, so far positions lose nothing.
 // Bound by HBM: every element is read and written once (262144 tokens, 8 + 8 heads,
-// bf16, backward: 183 us, 5.9 TB/s of the 6.5 that a copy reaches).
+// bf16, backward: 188-194 us, 5.5-5.7 TB/s of the 6.5 that a copy reaches; 32768 tokens of
+// 16 + 16 heads from a [B][L][H][d] projection 57 us, 4.7 TB/s, of which the kernel is 54:
+// a warp's loads there lie 2 KB apart, 64 to 128 bytes at a time).
 #include <cmath>
 #include <algorithm>
 
@@ -64,7 +66,7 @@ __device__ __forceinline__ void sincos_of(double p, double f, float& s, float& c
 template <typename T, int NP, bool HALF>
 __global__ void __launch_bounds__(256) k_rotary(const RotArgs a) {
     constexpr int NV = HALF ? NP : 2 * NP;  // elements of a piece
-    // bf16 has twice the pairs, and sines, in a thread (there 4 heads: 187 us for 183)
+    // bf16 has twice the pairs, and sines, in a thread (there 4 heads took 2 % longer)
     constexpr int U = sizeof(T) == 4 ? 4 : 1;
     const int t = blockIdx.x * blockDim.y + threadIdx.y, unit = threadIdx.x, b = blockIdx.z;
     if (t >= a.L) return;

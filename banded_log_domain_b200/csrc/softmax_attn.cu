@@ -64,7 +64,10 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     // The tensor-core forward's items are 4, 2 or 1 row tiles (see softmax_tc.cuh).
     // One leaves the fewest SMs idle where all tiles fit them at once; of many, two
     // share the key chunks (32768 tokens of 16 heads, W = 256: 187 us, four 191, one
-    // 237), and four pay once a tile's band is long (8192 dense tokens: 427 us, two 454).
+    // 237).  Four on long bands of many tiles: us with four and two on 8192 dense
+    // tokens 439, 465; 32768 with W = 4096 1436, 1469; 32768 causal ones of 4 key heads
+    // 2919, 2980.  Not everywhere: there are half as many items to share out (16384 dense
+    // tokens of 4 key heads 1664, 1529; 8191 causal ones 254, 235).
     pl->nr = 1;
     if (pl->tc && BH * RT > sms) pl->nr = W >= 4096 && BH * RT >= 6LL * sms ? 4 : 2;
     pl->per = pl->nr * pl->nq;
@@ -86,8 +89,9 @@ sa_status make_plan(const sa_softmax_params* p, Plan* pl) {
     long long parts = pl->nparts > 1 ? pl->rows * pl->nparts : 0;
     // Few query rows per key head are bound by reading the keys and
     // values: a kernel without tiles, whose blocks (two per SM, of two chunks or
-    // more) share all sequences' chunks evenly, takes 54 us where the tiled forward
-    // takes 85 (8 sequences of 32768 tokens, 4 key heads of 4 heads each, bf16).
+    // more) share all sequences' chunks evenly (4 key heads of 4 heads each, us here
+    // and tiled: 8 sequences of up to 32768 tokens, bf16 61, 86, fp32 152, 422; 64 of
+    // 8192, bf16 98, 199, fp32 244, 944).  Its limits on rows and sequences: see there.
     pl->token = 0;
     if ((long long)pl->G * p->Lq <= sm::token::max_rows(pl->tc) && p->B <= sm::token::MAXB && BH <= 4096 && BH > 0) {
         pl->token = (int)std::max<long long>(1, std::min<long long>(2LL * sms, BH * chunks / 2));

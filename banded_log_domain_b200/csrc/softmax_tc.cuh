@@ -88,8 +88,10 @@ struct Walk {
 // 2^x on the FMA pipe for a pair of arguments, x <= 8 or so: round to nearest by
 // adding 1.5 * 2^23, then a polynomial of degree 4 for 2^f on [-1/2, 1/2]
 // (least squares on Chebyshev nodes, reweighted towards the largest relative
-// error, which is 2.7e-6: a probability's rounding to bf16 is off by up to 2^-8
-// after it, and the row sums' duals keep 1e-5).
+// error, which is 2.7e-6).  Degree 4, where the row-sum sweeps of the Sinkhorn
+// iteration have 5: these exponentials enter one sum, not 2 T of them, a quarter of
+// them at that, so u is off by 2.7e-6 at most of the 1e-5 that duals keep; P is
+// rounded to bf16 next, off by up to 2^-8.
 __device__ __forceinline__ void exp2_poly2(uint64_t x, float& e0, float& e1) {
     float x0, x1;
     tc::upk2(x, x0, x1);
@@ -125,9 +127,13 @@ __device__ __forceinline__ uint32_t range_bits(int a, int b) {
 //   O += P V     128 x 64 x 64, P bf16 in TMEM over the S it came from
 // Four chains (S, exponentials, P V) in flight hide each other's latency: the
 // same kernel with two groups on chunks of 128 keys spent half its time in the
-// hand-overs.  8192 dense tokens of 8 heads take 231 us (tensor cores and the
-// exponentials alone 85 and 115): the exponential unit is 55 % busy, the tensor
-// cores 37 %, DRAM 1 %; the rest is a chain's hand-overs, S to P to O, and issue.
+// hand-overs.  8192 dense tokens of 8 heads take 235 us (tensor cores and the
+// exponentials alone 85 and 115): the exponential unit is 57 % busy, the tensor
+// cores 38 %, DRAM 1 %; the rest is a chain's hand-overs, S to P to O, and issue.
+// P is rounded to bf16 for P V: one MMA takes both operands in one type, V is bf16, and
+// P in two parts would double these products.  The sum of a row is that of the unrounded P in
+// fp32.  Against 64 bits O is off by 2.1e-3 to 2.4e-3 of its norm, 1.7e-3 of it the rounding of
+// O itself (which is all that is off where P stays fp32).
 // The running maximum is only moved when it has grown by more than 8 (in log2
 // units): until then probabilities are at most 2^8, which the fp32 sums and bf16's
 // exponent hold without loss, and O needs no rescaling.  The mask warp turns the
@@ -276,8 +282,9 @@ __global__ void __launch_bounds__(THREADS, 1) tc_fwd(const Args a, const __grid_
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
 
     // An item's slot is read in place and handed back to the loader at the item's
-    // end.  (Nothing of it may be indexed by a runtime value in registers: local
-    // memory would go to L2, as the shared memory leaves no L1 to speak of.)
+    // end.  (Nothing of it is indexed by a runtime value in registers: local memory
+    // would go to L2, as the shared memory leaves no L1 to speak of.  ptxas spills one
+    // register of a thread all the same.)
     auto begin_item = [&](int it) -> bool {
         return ctl.wait_warp(Y::IFULL + it % NIT, (it / NIT) & 1) && items[it % NIT].b >= 0;
     };

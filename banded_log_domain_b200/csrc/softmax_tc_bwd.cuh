@@ -31,7 +31,11 @@
 // dO . O is formed by the teams' warps at an item's start, a quarter of the channels
 // each.
 //
-// 8192 dense tokens of 8 heads take 651 us for the eight products, 0.52 of the
+// P and dS are rounded to bf16 for the second products (their other operands are
+// bf16; see softmax_tc.cuh); u, D, the sum of dS and all accumulators are fp32.  Gradients
+// are off by 2.4e-3 of their norm against 64 bits, 1.7e-3 of it their own rounding.
+//
+// 8192 dense tokens of 8 heads take 661 us for the eight products, 0.51 of the
 // matrix rate.  A banded item is bound by its start and its end, where the products
 // drain, a long one by the hand-overs.  (The row tiles' operands in TMEM as well
 // made the MMAs shorter but left five buffers of S or G in DKV: 3 % slower.)

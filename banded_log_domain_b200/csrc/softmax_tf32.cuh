@@ -4,7 +4,8 @@
 // Every fp32 operand is split in two tf32 numbers, x = hi + lo, hi rounded to
 // nearest and lo, of either sign, cut to 11 bits (at most 2^-21 of x is lost).
 // Every product is hi lo' + lo hi' + hi hi' with fp32 sums, the cross terms summed
-// apart; the term left out is 2^-22 of a product.  Against 64 bits the results are
+// apart; the term left out is 2^-22 of a product.  (hi of a magnitude from
+// 2^128 (1 - 2^-12) on rounds to infinity: such values count as infinite.)  Against 64 bits the results are
 // off by 3e-7 to 7e-7, as on the FMA pipe (6e-7).
 // mma.sync takes 508 tf32 FMA per clock and SM, a third of that here; two warps a
 // scheduler and the splitting keep it half busy.  Measured against 64 x 64 tiles on

@@ -11,7 +11,8 @@
 // kernel.
 //   bf16: warp-wide matrix instructions, S^T = K Q^T for 16 keys and 8 rows at a
 //     time and O^T += V^T P.  (tcgen05's 128 rows would be mostly empty, and its
-//     hand-overs took 1.5 times as long per byte.)
+//     hand-overs took 1.5 times as long per byte.)  P is rounded to bf16 for its
+//     product, as V is (see softmax_tc.cuh); the sum takes it unrounded.
 //   fp32: eight lanes hold a key's 64 channels, so a warp takes four keys at once,
 //     each with a softmax of its own; the sums of a score over eight lanes end
 //     each in one row's lanes, which alone go through that row's softmax.
@@ -26,8 +27,13 @@ namespace token {
 
 constexpr int THREADS = 256;     // fp32
 constexpr int THREADS_MMA = 128; // bf16
-constexpr int MAXB = 64;         // sequences (a loop over them finds a block's share)
-// query rows per key head
+// Sequences: a loop over them finds a block's share, and a warp's sum over them where they
+// lie.  The limit is a choice and not where the kernel stops paying: with it raised, 128
+// sequences of 8192 tokens took 168 us (tiled 377), 1024 of 1024 tokens 315 (394).
+constexpr int MAXB = 64;
+// Query rows per key head: what two tiles of eight (bf16), or four rows of eight lanes'
+// sums (fp32), hold.  The tiled forward takes more: 8 sequences of 8192 tokens, 8 key heads
+// of 8 heads, bf16: 16 rows 42 us here, 58 tiled; 24 rows 57 tiled.
 __host__ __device__ constexpr int max_rows(bool bf16) { return bf16 ? 16 : 4; }
 
 // Whether the sequences' chunks differ in number.

@@ -21,8 +21,9 @@
  *   dustbin row and one dustbin column (plus their corner) carrying the
  *   constant score dustbin_score, with unit mass like every other row/column.
  *
- * Debug build: compiled with -DSA_DEBUG (libsinkhorn_attn_debug.so) every
- * kernel of the Sinkhorn attention checks the indices of its guarded accesses (global rows and columns,
+ * Debug build: compiled with -DSA_DEBUG (libsinkhorn_attn_debug.so) every kernel
+ * of the Sinkhorn attention (not those of the softmax attention and the rotary
+ * positions) checks the indices of its guarded accesses (global rows and columns,
  * ring and buffer slots, tensor-memory columns, shared-memory offsets) before
  * making them; a failed check skips the access and records SA_ERR_BOUNDS in
  * the status word (read by sinkhorn_attn_poll).  Nothing traps.
@@ -381,7 +382,8 @@ sa_status sinkhorn_attn_bias_certificate(int n_depths, const int* depths, int n_
  * Lq = 1 with q_pos = (tokens held) - 1 is the step of a single new token over
  * a cache of capacity Lk.  A row with no key (masked, at a position outside
  * [0, Lk), or whose band is masked out) has O, u, dQ exactly 0; a key that no
- * query attends has dK, dV exactly 0.
+ * query attends has dK, dV exactly 0 (where no non-finite value reaches them, see
+ * below).
  *   - Q, O, dO, dQ are [B][Hq][Lq][d]; K, V, dK, dV [B][Hk][Lk][d]; each with
  *     element strides for batch, head and token (x_stride; three zeros:
  *     contiguous; the stride of an extent of 1 is not read), positive
@@ -395,7 +397,14 @@ sa_status sinkhorn_attn_bias_certificate(int n_depths, const int* depths, int n_
  *     P = exp(S + u) from the fp32 u, whose rounding is a factor of up to
  *     1 +- 2^-21 |u| on P: gradients take an error of that size and mean nothing
  *     from |u| of about 2^20 on.
- *   - Results do not depend on the order in which blocks run (no atomics).
+ *   - bf16: P and dS are rounded to bf16 in front of their products with V, K, Q
+ *     and dO; maxima, sums, u and accumulators are fp32.  fp32: products of operands
+ *     split in two tf32 parts, a term off by 1.3 2^-20 at most.
+ *   - Results do not depend on the order in which blocks run (no atomics): a call
+ *     gives the same bits again.  They do depend on the sizes: how many row tiles
+ *     share a block's keys, and in how many parts a row's keys are taken, goes by
+ *     the number of tiles of the whole call, so that a head alone and the same head
+ *     in a larger batch may differ within the roundings above.
  *   - The workspace needs no initialisation: every call resets the status word
  *     at its start (read it with sinkhorn_attn_poll), so calls on two streams
  *     at once, or captured into graphs that may run at once, need one each.
