@@ -793,6 +793,8 @@ def sinkhorn_attn_rotary_freqs(rot, *, base=10000.0, scaling="plain", factor=1.0
     position) and ``scale`` the factor to pass along.  ``scaling``: "plain", or
     stretched by ``factor`` for contexts longer than the trained one: "linear",
     "ntk", "by_parts" (with ``train_len`` and ``turns``, see the C header)."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling: one of {', '.join(ROTARY_SCALINGS)}, not {scaling!r}")
     n = max(int(rot) // 2, 1)
     out, scale = (ctypes.c_double * n)(), ctypes.c_float(1.0)
     _check(_L().sinkhorn_attn_rotary_freqs(int(rot), float(base), ROTARY_SCALINGS[scaling],
@@ -805,6 +807,8 @@ def sinkhorn_attn_rotary_freqs(rot, *, base=10000.0, scaling="plain", factor=1.0
 def _rotary(entry, q, k, freqs, pos, interleaved, scale, q_out, k_out):
     if q.dim() != 4 or not q.is_cuda or q.dtype not in _DTYPES:
         raise ValueError("q, k are [B,H,L,d] float32 or bfloat16 CUDA tensors")
+    if not isinstance(freqs, torch.Tensor):
+        raise ValueError("freqs: the tensor that sinkhorn_attn_rotary_freqs returns first")
     B, Hq, L, d = q.shape
     dev, Hk, pk, pko = q.device, 0, None, None
     if k is not None:

@@ -204,6 +204,12 @@ def test_rotary_frequencies_refuse(kw):
     assert e.value.status == -1
 
 
+def test_unknown_scalings_are_refused():
+    for scaling in ("none", "yarn", None, 2):
+        with pytest.raises(ValueError, match="by_parts"):
+            sa.sinkhorn_attn_rotary_freqs(64, scaling=scaling, device="cpu")
+
+
 def test_python_checks():
     q = torch.zeros(1, 2, 4, 64)
     with pytest.raises(ValueError):

@@ -511,6 +511,15 @@ def test_cosines_and_sines_at_far_positions(inverse):
     assert float((y - want).abs().max()) <= 5 * 2.0 ** -24
 
 
+def test_rotary_refuses_the_pair_of_frequencies_and_factor():
+    import banded_log_domain_b200 as sa
+
+    q = torch.zeros(1, 1, 4, 64, device="cuda")
+    for f in (sa.sinkhorn_attn_rotary_fwd, sa.sinkhorn_attn_rotary_bwd):
+        with pytest.raises(ValueError, match="freqs"):
+            f(q, q, sa.sinkhorn_attn_rotary_freqs(64))
+
+
 def test_rotary_is_relative():
     # the scores of rotated queries and keys depend on the distance alone
     import banded_log_domain_b200 as sa
