@@ -535,6 +535,50 @@ def test_rotary_is_relative():
     assert float((s[0] - s[1]).abs().max()) <= 64 * 25 * 2.0 ** -20
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rotary_in_a_graph_and_on_two_streams(dtype):
+    import banded_log_domain_b200 as sa
+
+    freqs, _ = sa.sinkhorn_attn_rotary_freqs(64)
+    probs = [draw(dtype, 2, 4, 2, L, L, seed=L)[:2] for L in (1, 3000)]
+    pos = [torch.full((2, 1), 70000, dtype=torch.int32, device="cuda"), None]
+
+    def step(x, p):
+        y = sa.sinkhorn_attn_rotary_fwd(*x, freqs, pos=p)
+        return y + sa.sinkhorn_attn_rotary_bwd(*y, freqs, pos=p)
+
+    want = [step(*z) for z in zip(probs, pos)]
+    streams = [torch.cuda.Stream() for _ in probs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(3):
+        for s, x, p in zip(streams, probs, pos):
+            with torch.cuda.stream(s):
+                got.append(step(x, p))
+    torch.cuda.synchronize()
+    for n, y in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(y, want[n % 2]))
+    for x, p, w in zip(probs, pos, want):
+        live = [t.clone() for t in x]
+        at = None if p is None else p.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step(live, at)
+        for t in live:
+            t.neg_()
+        if at is not None:
+            at.add_(5)
+        graph.replay()
+        for t, y in zip(live, x):
+            t.copy_(y)
+        if at is not None:
+            at.copy_(p)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, w))
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("dtype", TYPES)
 def test_a_layer_rotary_attention_and_back(dtype):
