@@ -152,6 +152,30 @@ def test_scores_of_any_size(dtype, log2_eps, Hq, Lq, Lk, W):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("eps", [2.0 ** -4, 2.0 ** -7])
+def test_gradients_at_large_duals(dtype, eps, monkeypatch):
+    # P = exp(S + u) from an fp32 u: u passes seven roundings on its way from the maximum to
+    # the exponent (c2, the product, the sum, ln 2 and its product, 1 / c, c2 again), 2^-21 |u|
+    # in all; the score's own, of 64 terms of random sign, 8 2^-24 sum |q k| c, is under
+    # 2^-21 of |u| plus that sum / 8.  Twice that for P in the forward and here.
+    import banded_log_domain_b200 as sa
+
+    q, k, v, dO = draw(dtype, 1, 4, 2, 260, 260, seed=31)
+    kw = dict(W=90, causal=True)
+    o, u = sa.sinkhorn_attn_softmax_fwd(q, k, v, eps=eps, **kw)
+    wo, wu, P = ref.forward(q, k, v, eps=eps, **kw)
+    terms = (q.double().abs() @ k.double().abs().repeat_interleave(2, 1).transpose(-1, -2)).max() / (8 * eps)
+    s = float(wu.abs().max() + terms / 8) * 2.0 ** -21
+    assert float((u.double() - wu).abs().max()) <= s
+    monkeypatch.setattr(ref, "S", 2 * s)
+    lim = ref.bounds(q, k, v, dO, P, dtype, eps=eps)
+    ref.close("o", o, wo, lim["o"], dtype)
+    got = sa.sinkhorn_attn_softmax_bwd(q, k, v, o, dO, u, eps=eps, **kw)
+    for n, x, w in zip(("dq", "dk", "dv"), got, ref.backward(q, k, v, dO, P, eps=eps)):
+        ref.close(n, x, w, lim[n], dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("G", [1, 4, 7])
 @pytest.mark.parametrize("Lq,Lk,W", [(1, 1, 0), (1, 70, 70), (1, 1000, 1000), (1, 5000, 5000), (1, 5000, 300),
                                      (2, 130, 130), (5, 4096, 4096), (17, 3001, 3001), (40, 3001, 900)])
